@@ -69,7 +69,9 @@ typedef enum {
                              vocabulary; those rows got no delta, the rest are valid */
 } lora_status;
 
-typedef enum { LORA_F32 = 0, LORA_BF16 = 1 } lora_dtype;
+/* LORA_MXFP4 (experts' weights and their inputs only): the microscaled 4-bit
+ * format of lora_mx_quantize. */
+typedef enum { LORA_F32 = 0, LORA_BF16 = 1, LORA_MXFP4 = 2 } lora_dtype;
 
 /* Which kernel family runs a shrink / expand.
  * BGMV: per-segment streaming of each adapter's A/B on CUDA cores (decode).
@@ -99,6 +101,9 @@ typedef enum { LORA_AUTO = 0, LORA_BGMV = 1, LORA_SGMV = 2, LORA_MIXED = 3 } lor
 #define LORA_MAX_NUM_SLOTS 1024
 #define LORA_MAX_RANK 128
 #define LORA_MAX_TOKENS (1 << 24)
+#define LORA_MAX_EXPERTS 1024      /* lora_moe_route: experts of a layer */
+#define LORA_MAX_ROUTE_TOPK 32     /* lora_moe_route: choices of a token */
+#define LORA_MX_BLOCK 32           /* elements that share a scale in the 4-bit format */
 #define LORA_SGMV_MIN_ROWS 32      /* AUTO threshold: segment rows routed to SGMV */
 #define LORA_SGMV_TILE_M 128       /* rows per SGMV tile (work-list granularity) */
 #define LORA_AUTO_SGMV_MIN_TOKENS 1024  /* AUTO: smaller batches run all on BGMV */
@@ -324,6 +329,165 @@ size_t lora_meta_tiles_bytes(int32_t num_slots);
 int lora_moe_pair_slots(const int32_t *token_slot, const int32_t *topk_ids, int32_t num_tokens, int32_t topk,
                         int32_t num_loras, int32_t num_experts, int32_t local_experts, const int32_t *expert_map,
                         int32_t *pair_slot, lora_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The mixture-of-experts layer around its LoRA. The multi-LoRA pages take the
+ * experts chosen, the base outputs of w13 and w2 and the sum over the choices
+ * as given; the calls below compute them on the same pairs, row order and
+ * metadata as the LoRA calls, so that a layer runs as
+ *   lora_moe_route -> lora_moe_pair_slots, lora_prepare_meta (twice: the pairs
+ *   by expert for the products, by (adapter, expert) for the LoRA) ->
+ *   lora_moe_product (w13) -> lora_apply (w13) -> lora_moe_act ->
+ *   lora_moe_product (w2) -> lora_apply (w2) -> lora_moe_combine.
+ * Pairs are token-major, pair p = t * topk + k. A pair's product slot is
+ * 1 + its local expert, or 0 when no expert of this rank serves it; rows of
+ * slot-0 pairs are neither read nor written. All buffers follow the
+ * conventions at the top of this file: every kernel waits for its predecessor
+ * before it reads anything.
+ * ------------------------------------------------------------------------ */
+
+/* Weight of a chosen expert from its logit l (lora_moe_route). */
+typedef enum { LORA_SCORE_SOFTMAX = 0, LORA_SCORE_SIGMOID = 1 } lora_score;
+
+/*
+ * Router: each token's topk experts with the largest logits, in descending
+ * order, ties to the lowest expert, and their weights:
+ *   LORA_SCORE_SOFTMAX  exp(l - m) / sum over all experts of exp(l - m)
+ *   LORA_SCORE_SIGMOID  1 / (1 + exp(-l))
+ * divided by their sum over the token's choices when renormalize is non-zero,
+ * then multiplied by scale. A logit of -infinity or NaN excludes its expert:
+ * it is chosen only when fewer than topk others are left (lowest expert
+ * first), with weight 0; a row that excludes every expert has weights 0.
+ * +infinity counts as the largest finite number.
+ *   logits:     device, [num_tokens, num_experts], row stride ld_logits
+ *               elements, LORA_F32 or LORA_BF16; no alignment beyond the type's
+ *   topk_ids:   device int32 [num_tokens * topk]
+ *   topk_w:     device fp32 [num_tokens * topk]
+ *   pair_slot:  device int32 [num_tokens * topk] or NULL: the pairs' product
+ *               slots, 1 + expert_map[e] (as lora_moe_pair_slots for a token of
+ *               adapter 1), 0 for an expert held elsewhere (expert_map[e] < 0)
+ *               or an excluded choice, -1 where expert_map[e] >= local_experts.
+ *               May be the token_slot of a lora_meta prepared next.
+ *   expert_map: device int32 [num_experts], or NULL (every expert is local)
+ * Sums and weights are formed in fp32. Errors: null logits, topk_ids or
+ * topk_w, or an unknown dtype or score -> LORA_EINVAL; num_tokens outside
+ * [0, LORA_MAX_TOKENS / topk], num_experts outside [1, LORA_MAX_EXPERTS], topk
+ * outside [1, min(num_experts, LORA_MAX_ROUTE_TOPK)] or (with pair_slot)
+ * local_experts outside [1, num_experts] -> LORA_ERANGE; ld_logits <
+ * num_experts -> LORA_EINVAL; misaligned arrays -> LORA_EALIGN.
+ */
+int lora_moe_route(const void *logits, int64_t ld_logits, int32_t dtype, int32_t num_tokens, int32_t num_experts,
+                   int32_t topk, int32_t score, int32_t renormalize, float scale, const int32_t *expert_map,
+                   int32_t local_experts, int32_t *topk_ids, float *topk_w, int32_t *pair_slot, lora_stream_t stream);
+
+/*
+ * The weights of one projection of a layer's local experts, one row an output:
+ *   W: device, [num_experts, d_out, d_in] row-major, d_in contiguous. LORA_F32
+ *      (accuracy runs), LORA_BF16, or LORA_MXFP4: two elements a byte as
+ *      lora_mx_quantize writes them, d_in / 2 bytes a row.
+ *   W_scale, ld_scale: LORA_MXFP4 only: scale bytes [num_experts, d_out] rows
+ *      of ld_scale bytes (d_in / LORA_MX_BLOCK of them used).
+ *   x_row_div: pair p reads x row p / x_row_div (0 or 1: row p), as in
+ *      lora_layer_desc; a w13 projection sets topk.
+ * Constraints: 1 <= num_experts < LORA_MAX_NUM_SLOTS; d_in and d_out positive
+ * multiples of 8 (d_in of LORA_MX_BLOCK for LORA_MXFP4); W and W_scale 16-byte
+ * aligned, ld_scale a multiple of 16 and at least d_in / LORA_MX_BLOCK.
+ */
+typedef struct {
+  int32_t dtype;
+  int32_t d_in;
+  int32_t d_out;
+  int32_t num_experts;
+  const void *W;
+  const uint8_t *W_scale;
+  int64_t ld_scale;
+  int32_t x_row_div;
+} lora_expert_desc;
+
+/*
+ * The experts' product: for every pair p whose slot s = token_slot[p] != 0,
+ *   y[p, n] = sum_j x[p / x_row_div, j] * W[s - 1][n, j]       (n < d_out)
+ * Products of bf16 and of 4-bit operands are exact, sums are fp32, the result
+ * is rounded once. y is overwritten, not added to; rows of slot-0 pairs are
+ * left alone. Results do not depend on the batch's other pairs' values and
+ * repeat bitwise.
+ *   meta: lora_prepare_meta over the pairs' product slots; its num_slots is
+ *         desc->num_experts + 1, its num_tokens the number of pairs
+ *   x:    device, [ceil(num_tokens / x_row_div), d_in], row stride ldx
+ *         elements, of desc->dtype (LORA_MXFP4: rows of codes, ldx / 2 bytes
+ *         apart, with x_scale rows of ld_xscale bytes)
+ *   y:    device, [num_tokens, d_out], row stride ldy, LORA_F32 or LORA_BF16
+ * Errors: null pointers, ldx < d_in, ldy < d_out, a slot count that differs,
+ * ld_xscale too small -> LORA_EINVAL; an fp32 table with a bf16 y ->
+ * LORA_EUNSUPPORTED; a pointer or row stride that is not a multiple of 16
+ * bytes -> LORA_EALIGN. A kernel that gave up waiting on its pipeline is
+ * reported by lora_query_status(meta) as LORA_EDEVICE.
+ */
+int lora_moe_product(const lora_expert_desc *desc, const lora_meta *meta, const void *x, int64_t ldx,
+                     const uint8_t *x_scale, int64_t ld_xscale, void *y, int64_t ldy, int32_t y_dtype,
+                     lora_stream_t stream);
+
+/*
+ * Rows to the microscaled 4-bit format. Each block of LORA_MX_BLOCK
+ * consecutive elements of a row gets the scale 2^e, e = floor(log2 max|x|) - 2
+ * held to [-127, 127] (e = -127 for a block of zeros), stored as the byte
+ * e + 127; each element the e2m1 code (values 0, .5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives) nearest to x * 2^-e, ties to the even code, magnitudes
+ * above 6 to 6. Element 2i is in the low four bits of byte i. A block that
+ * holds a NaN or an infinity gets byte 255 (NaN) and codes 0.
+ *   x:      device, [rows, cols], row stride ldx elements, LORA_F32 or
+ *           LORA_BF16; cols a positive multiple of LORA_MX_BLOCK
+ *   codes:  device, [rows, cols / 2] bytes, row stride ld_codes bytes
+ *   scales: device, [rows, cols / LORA_MX_BLOCK] bytes, row stride ld_scales
+ *           bytes; bytes past a row's blocks are left alone
+ * Pointers and row strides in bytes are multiples of 16 (else LORA_EALIGN).
+ * rows == 0 is a no-op; rows < 0 -> LORA_ERANGE.
+ */
+int lora_mx_quantize(const void *x, int64_t ldx, int32_t x_dtype, int64_t rows, int32_t cols, uint8_t *codes,
+                     int64_t ld_codes, uint8_t *scales, int64_t ld_scales, lora_stream_t stream);
+
+/* The values that codes and scales stand for, y[r, c] = code * 2^(byte - 127)
+ * (exact in LORA_F32 and LORA_BF16; byte 255 gives NaN). Arguments and errors
+ * as lora_mx_quantize. */
+int lora_mx_dequantize(const uint8_t *codes, int64_t ld_codes, const uint8_t *scales, int64_t ld_scales, int64_t rows,
+                       int32_t cols, void *y, int64_t ldy, int32_t y_dtype, lora_stream_t stream);
+
+/*
+ * The gated activation between w13 and w2, for every pair with pair_slot > 0
+ * (every row when pair_slot is NULL; other rows are left alone):
+ *   h[p, i] = silu(y13[p, i]) * y13[p, inter + i]        silu(g) = g / (1 + exp(-g))
+ * in fp32, rounded once.
+ *   y13: device, [num_pairs, 2 * inter], row stride ldy elements, LORA_F32 or
+ *        LORA_BF16; inter a positive multiple of 8
+ *   h:   device, [num_pairs, inter], row stride ldh elements, LORA_F32 or LORA_BF16
+ * Alignment as elsewhere: pointers and row strides multiples of 16 bytes,
+ * pair_slot of 4.
+ */
+int lora_moe_act(const void *y13, int64_t ldy, int32_t y_dtype, const int32_t *pair_slot, int32_t num_pairs,
+                 int32_t inter, void *h, int64_t ldh, int32_t h_dtype, lora_stream_t stream);
+
+/* lora_moe_act into bf16 followed by lora_mx_quantize, in one pass and bitwise
+ * the same: the 4-bit input of a w2 product. inter a positive multiple of
+ * LORA_MX_BLOCK; codes and scales as lora_mx_quantize writes them. */
+int lora_moe_act_mx(const void *y13, int64_t ldy, int32_t y_dtype, const int32_t *pair_slot, int32_t num_pairs,
+                    int32_t inter, uint8_t *codes, int64_t ld_codes, uint8_t *scales, int64_t ld_scales,
+                    lora_stream_t stream);
+
+/*
+ * The weighted sum over a token's choices:
+ *   out[t, n] = (accumulate ? out[t, n] : 0) + sum_k topk_w[t * topk + k] * y[t * topk + k, n]
+ * over the choices with pair_slot > 0 (all when pair_slot is NULL), in fp32 in
+ * the order of k, rounded once. A token without such a choice gets 0 (or
+ * keeps out).
+ *   y:   device, [num_tokens * topk, n], row stride ldy, LORA_F32 or LORA_BF16
+ *   out: device, [num_tokens, n], row stride ldo, LORA_F32 or LORA_BF16; must
+ *        not overlap y
+ * n a positive multiple of 8; topk outside [1, 64] or num_tokens outside
+ * [0, LORA_MAX_TOKENS / topk] -> LORA_ERANGE.
+ */
+int lora_moe_combine(const void *y, int64_t ldy, int32_t y_dtype, const float *topk_w, const int32_t *pair_slot,
+                     int32_t num_tokens, int32_t topk, int32_t n, void *out, int64_t ldo, int32_t out_dtype,
+                     int32_t accumulate, lora_stream_t stream);
 
 /*
  * Synchronise `stream`, copy meta->status to *out (host) and return

@@ -29,6 +29,10 @@ __all__ = [
     "lora_set_slot", "lora_reset_slot", "lora_prepare_meta", "lora_prepare_meta_unshared", "lora_shrink", "lora_expand", "lora_apply",
     "lora_shrink_noalloc", "lora_noalloc_scratch_bytes", "lora_embed_shrink", "embed_shrink",
     "lora_moe_pair_slots", "moe_pair_slots",
+    "LORA_MXFP4", "LORA_SCORE_SOFTMAX", "LORA_SCORE_SIGMOID", "LORA_MAX_EXPERTS", "LORA_MAX_ROUTE_TOPK", "LORA_MX_BLOCK",
+    "lora_moe_route", "lora_moe_product", "lora_mx_quantize", "lora_mx_dequantize", "lora_moe_act", "lora_moe_act_mx",
+    "lora_moe_combine", "ExpertDesc", "ExpertWeights", "moe_route", "moe_product", "mx4_buffers", "mx4_quantize",
+    "mx4_dequantize", "moe_act", "moe_act_mx4", "moe_combine",
     "lora_workspace_bytes", "lora_meta_tiles_bytes", "lora_query_status", "lora_probe_bounded_wait", "lora_strerror",
     "lora_last_cuda_error", "lora_launch_count", "SlotTable", "TokenMeta", "shrink", "expand", "apply", "workspace", "check",
 ]
@@ -37,6 +41,11 @@ __all__ = [
  LORA_EBADTOKEN) = range(9)
 LORA_F32, LORA_BF16 = 0, 1
 LORA_AUTO, LORA_BGMV, LORA_SGMV, LORA_MIXED = 0, 1, 2, 3
+LORA_MXFP4 = 2                                  # experts' weights and inputs only
+LORA_SCORE_SOFTMAX, LORA_SCORE_SIGMOID = 0, 1
+LORA_MAX_EXPERTS = 1024
+LORA_MAX_ROUTE_TOPK = 32
+LORA_MX_BLOCK = 32
 LORA_MAX_SLICES = 4
 LORA_MAX_NUM_SLOTS = 1024
 LORA_MAX_RANK = 128
@@ -85,6 +94,15 @@ class Meta(ctypes.Structure):
     ]
 
 
+class ExpertDesc(ctypes.Structure):
+    """lora_expert_desc: one projection's expert weights (device pointers)."""
+    _fields_ = [
+        ("dtype", _i32), ("d_in", _i32), ("d_out", _i32), ("num_experts", _i32),
+        ("W", _vp), ("W_scale", _vp), ("ld_scale", ctypes.c_int64), ("x_row_div", _i32),
+    ]
+
+
+_i64 = ctypes.c_int64
 _P = ctypes.POINTER
 _sig = {
     "lora_set_slot": (_i32, [_P(LayerDesc), _i32, _i32, ctypes.c_float, _P(_vp), _P(_vp), _vp]),
@@ -103,6 +121,14 @@ _sig = {
     "lora_probe_bounded_wait": (_i32, [_P(Meta), ctypes.c_uint32, _vp]),
     "lora_embed_shrink": (_i32, [_P(LayerDesc), _P(Meta), _vp, _vp, _vp]),
     "lora_moe_pair_slots": (_i32, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "lora_moe_route": (_i32, [_vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _vp, _i32, _vp, _vp, _vp,
+                              _vp]),
+    "lora_moe_product": (_i32, [_P(ExpertDesc), _P(Meta), _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp]),
+    "lora_mx_quantize": (_i32, [_vp, _i64, _i32, _i64, _i32, _vp, _i64, _vp, _i64, _vp]),
+    "lora_mx_dequantize": (_i32, [_vp, _i64, _vp, _i64, _i64, _i32, _vp, _i64, _i32, _vp]),
+    "lora_moe_act": (_i32, [_vp, _i64, _i32, _vp, _i32, _i32, _vp, _i64, _i32, _vp]),
+    "lora_moe_act_mx": (_i32, [_vp, _i64, _i32, _vp, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
+    "lora_moe_combine": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _i64, _i32, _i32, _vp]),
     "lora_strerror": (ctypes.c_char_p, [_i32]),
     "lora_last_cuda_error": (_i32, []),
     "lora_launch_count": (ctypes.c_uint64, []),
@@ -191,6 +217,52 @@ def lora_moe_pair_slots(token_slot: int, topk_ids: int, num_tokens: int, topk: i
     """Composite (adapter, local expert) slot of every (token, choice) pair (see the header)."""
     return _lib.lora_moe_pair_slots(token_slot, topk_ids, num_tokens, topk, num_loras, num_experts, local_experts,
                                     expert_map, pair_slot, _stream(stream))
+
+
+def lora_moe_route(logits: int, ld_logits: int, dtype: int, num_tokens: int, num_experts: int, topk: int, score: int,
+                   renormalize: bool, scale: float, expert_map: int, local_experts: int, topk_ids: int, topk_w: int,
+                   pair_slot: int, stream=None) -> int:
+    """Router: topk experts of every token, their weights and (pair_slot) the pairs' product slots."""
+    return _lib.lora_moe_route(logits or None, ld_logits, dtype, num_tokens, num_experts, topk, score,
+                               int(bool(renormalize)), scale, expert_map or None, local_experts, topk_ids or None,
+                               topk_w or None, pair_slot or None, _stream(stream))
+
+
+def lora_moe_product(desc: ExpertDesc, meta: Meta, x: int, ldx: int, x_scale: int, ld_xscale: int, y: int, ldy: int,
+                     y_dtype: int, stream=None) -> int:
+    """y[p] = x[p / x_row_div] . W[slot p - 1]^T for pairs with a slot (see the header)."""
+    return _lib.lora_moe_product(ctypes.byref(desc), ctypes.byref(meta), x or None, ldx, x_scale or None, ld_xscale,
+                                 y or None, ldy, y_dtype, _stream(stream))
+
+
+def lora_mx_quantize(x: int, ldx: int, x_dtype: int, rows: int, cols: int, codes: int, ld_codes: int, scales: int,
+                     ld_scales: int, stream=None) -> int:
+    return _lib.lora_mx_quantize(x or None, ldx, x_dtype, rows, cols, codes or None, ld_codes, scales or None,
+                                 ld_scales, _stream(stream))
+
+
+def lora_mx_dequantize(codes: int, ld_codes: int, scales: int, ld_scales: int, rows: int, cols: int, y: int, ldy: int,
+                       y_dtype: int, stream=None) -> int:
+    return _lib.lora_mx_dequantize(codes or None, ld_codes, scales or None, ld_scales, rows, cols, y or None, ldy,
+                                   y_dtype, _stream(stream))
+
+
+def lora_moe_act(y13: int, ldy: int, y_dtype: int, pair_slot: int, num_pairs: int, inter: int, h: int, ldh: int,
+                 h_dtype: int, stream=None) -> int:
+    return _lib.lora_moe_act(y13 or None, ldy, y_dtype, pair_slot or None, num_pairs, inter, h or None, ldh, h_dtype,
+                             _stream(stream))
+
+
+def lora_moe_act_mx(y13: int, ldy: int, y_dtype: int, pair_slot: int, num_pairs: int, inter: int, codes: int,
+                    ld_codes: int, scales: int, ld_scales: int, stream=None) -> int:
+    return _lib.lora_moe_act_mx(y13 or None, ldy, y_dtype, pair_slot or None, num_pairs, inter, codes or None, ld_codes,
+                                scales or None, ld_scales, _stream(stream))
+
+
+def lora_moe_combine(y: int, ldy: int, y_dtype: int, topk_w: int, pair_slot: int, num_tokens: int, topk: int, n: int,
+                     out: int, ldo: int, out_dtype: int, accumulate: bool = False, stream=None) -> int:
+    return _lib.lora_moe_combine(y or None, ldy, y_dtype, topk_w or None, pair_slot or None, num_tokens, topk, n,
+                                 out or None, ldo, out_dtype, int(bool(accumulate)), _stream(stream))
 
 
 def lora_shrink_noalloc(desc: LayerDesc, meta: Meta, x: int, ldx: int, buf: int, stream=None) -> int:
@@ -405,3 +477,194 @@ def apply(table: SlotTable, meta: TokenMeta, x, y, buf=None, kind: int = LORA_AU
     wsp, wsb, _keep = _ws_args(table, meta, kind, ws)
     check(lora_apply(table.desc, meta.c, x.data_ptr(), x.stride(0), buf.data_ptr() if buf is not None else 0,
                      y.data_ptr(), y.stride(0), ydt, kind, wsp, wsb, stream), "lora_apply")
+
+
+# ----------------------------------------------------------------------------- the MoE layer around its LoRA
+
+def _dt(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return LORA_BF16
+    if t.dtype == torch.float32:
+        return LORA_F32
+    raise TypeError(f"expected a bf16 or fp32 tensor, got {t.dtype}")
+
+
+def _rows(t, width: int, name: str, dtypes=None):
+    """(data pointer, row stride) of a 2-D tensor whose rows are contiguous and ``width`` wide."""
+    if t.dim() != 2 or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected [rows, {width}] with contiguous rows, got shape {tuple(t.shape)}, "
+                         f"strides {t.stride()}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype}")
+    # A single row's stride means nothing (torch may report any value): its length, rounded to the ABI's 16 bytes.
+    es = t.element_size()
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else -(-width * es // 16) * 16 // es
+
+
+def _vec(t, n: int, name: str, dtype):
+    """Data pointer of a contiguous tensor of n elements (0 for None)."""
+    if t is None:
+        return 0
+    if t.numel() != n or not t.is_contiguous() or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {n} contiguous {dtype} elements, got {tuple(t.shape)} {t.dtype}")
+    return t.data_ptr()
+
+
+class ExpertWeights:
+    """The local experts' weights of one projection, in caller-owned torch memory.
+
+    ``w``: [num_experts, d_out, d_in] bf16 or fp32, or the 4-bit codes [num_experts, d_out, d_in / 2]
+    uint8 with ``scale`` [num_experts, d_out, ld] uint8 (``mx4_quantize`` of the weights' rows). ``x_row_div``:
+    pair p reads x row p // x_row_div (a w13 projection: topk).
+    """
+
+    def __init__(self, w, scale=None, x_row_div: int = 1):
+        import torch
+        if w.dim() != 3 or not w.is_contiguous():
+            raise ValueError(f"ExpertWeights: expected contiguous [experts, d_out, d_in] weights, got {tuple(w.shape)}")
+        d = ExpertDesc()
+        d.num_experts, d.d_out, d.d_in = w.shape
+        if scale is not None:
+            if w.dtype != torch.uint8 or scale.dtype != torch.uint8 or not scale.is_contiguous() \
+                    or scale.shape[:2] != w.shape[:2]:
+                raise ValueError("ExpertWeights: 4-bit weights are uint8 codes [experts, d_out, d_in / 2] and contiguous "
+                                 "uint8 scales [experts, d_out, ld]")
+            d.dtype, d.d_in = LORA_MXFP4, 2 * w.shape[2]
+            d.W_scale, d.ld_scale = scale.data_ptr(), scale.shape[2]
+        else:
+            d.dtype = _dt(w)
+        d.W, d.x_row_div = w.data_ptr(), x_row_div
+        self.w, self.scale, self.desc = w, scale, d
+
+    @property
+    def d_in(self) -> int:
+        return self.desc.d_in
+
+    @property
+    def d_out(self) -> int:
+        return self.desc.d_out
+
+    def nbytes(self) -> int:
+        return self.w.numel() * self.w.element_size() + (self.scale.numel() if self.scale is not None else 0)
+
+
+_SCORES = {"softmax": LORA_SCORE_SOFTMAX, "sigmoid": LORA_SCORE_SIGMOID}
+
+
+def moe_route(logits, topk: int, score="softmax", renormalize: bool = True, scale: float = 1.0, expert_map=None,
+              local_experts: Optional[int] = None, topk_ids=None, topk_w=None, pair_slot=None, stream=None):
+    """(topk_ids int32 [T, topk], topk_w fp32 [T, topk]) for logits [T, E] (see lora_moe_route).
+
+    ``pair_slot`` (int32 [T * topk]): when given, also receives the pairs' product slots."""
+    import torch
+    T, E = int(logits.shape[0]), int(logits.shape[1])
+    lp, ld = _rows(logits, E, "logits")
+    if topk_ids is None:
+        topk_ids = torch.empty(T, topk, dtype=torch.int32, device=logits.device)
+    if topk_w is None:
+        topk_w = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
+    check(lora_moe_route(lp, max(ld, E), _dt(logits), T, E, topk, _SCORES.get(score, score), renormalize, scale,
+                         _vec(expert_map, E, "expert_map", torch.int32), E if local_experts is None else local_experts,
+                         _vec(topk_ids, T * topk, "topk_ids", torch.int32), _vec(topk_w, T * topk, "topk_w", torch.float32),
+                         _vec(pair_slot, T * topk, "pair_slot", torch.int32), stream), "lora_moe_route")
+    return topk_ids, topk_w
+
+
+def moe_product(experts: ExpertWeights, meta: TokenMeta, x, y, x_scale=None, stream=None) -> None:
+    """y[p] = x[p // x_row_div] @ W[slot p - 1].T for the pairs with a slot (see lora_moe_product).
+
+    ``meta``: prepared over the pairs' product slots. x: [rows, d_in] of the weights' type; with 4-bit weights
+    the codes [rows, d_in / 2] and ``x_scale`` [rows, ld] of mx4_quantize."""
+    d, P = experts.desc, meta.c.num_tokens
+    mx = d.dtype == LORA_MXFP4
+    if not mx and _dt(x) != d.dtype or mx and (x.element_size() != 1 or x_scale is None):
+        raise TypeError(f"moe_product: x of {x.dtype} does not go with the experts' weights")
+    xp, ldx = _rows(x, d.d_in // 2 if mx else d.d_in, "x")
+    need = -(-P // max(1, d.x_row_div))
+    if x.shape[0] < need or y.shape[0] < P:
+        raise ValueError(f"moe_product: {P} pairs need {need} rows of x and {P} of y, got {x.shape[0]} and {y.shape[0]}")
+    sp, lds = 0, 0
+    if mx:
+        sp, lds = _rows(x_scale, x_scale.shape[1], "x_scale")
+        if x_scale.shape[0] < need:
+            raise ValueError(f"moe_product: {need} rows of x_scale needed, got {x_scale.shape[0]}")
+        ldx *= 2
+    yp, ldy = _rows(y, d.d_out, "y")
+    check(lora_moe_product(d, meta.c, xp, ldx, sp, lds, yp, ldy, _dt(y), stream), "lora_moe_product")
+
+
+def mx4_buffers(rows: int, cols: int, device="cuda"):
+    """Codes [rows, cols / 2] and scale bytes [rows, cols / 32 rounded up to 16] for mx4_quantize."""
+    import torch
+    return (torch.empty(rows, cols // 2, dtype=torch.uint8, device=device),
+            torch.empty(rows, -(-cols // LORA_MX_BLOCK // 16) * 16, dtype=torch.uint8, device=device))
+
+
+def mx4_quantize(x, codes=None, scales=None, stream=None):
+    """(codes, scales) of the rows of x [rows, cols] in the microscaled 4-bit format (see lora_mx_quantize)."""
+    rows, cols = int(x.shape[0]), int(x.shape[1])
+    if codes is None or scales is None:
+        c, s = mx4_buffers(rows, cols, x.device)
+        codes, scales = c if codes is None else codes, s if scales is None else scales
+    xp, ldx = _rows(x, cols, "x")
+    cp, ldc, sp, lds = _mx_ptrs(codes, scales, rows, cols)
+    check(lora_mx_quantize(xp, ldx, _dt(x), rows, cols, cp, ldc, sp, lds, stream), "lora_mx_quantize")
+    return codes, scales
+
+
+def mx4_dequantize(codes, scales, y, stream=None):
+    """y [rows, cols] = the values that codes and scales stand for (see lora_mx_dequantize)."""
+    rows, cols = int(y.shape[0]), int(y.shape[1])
+    yp, ldy = _rows(y, cols, "y")
+    cp, ldc, sp, lds = _mx_ptrs(codes, scales, rows, cols)
+    check(lora_mx_dequantize(cp, ldc, sp, lds, rows, cols, yp, ldy, _dt(y), stream), "lora_mx_dequantize")
+    return y
+
+
+def _mx_ptrs(codes, scales, rows: int, cols: int):
+    import torch
+    cp, ldc = _rows(codes, cols // 2, "codes", (torch.uint8,))
+    sp, lds = _rows(scales, scales.shape[1], "scales", (torch.uint8,))
+    if codes.shape[0] < rows or scales.shape[0] < rows:
+        raise ValueError(f"{rows} rows need as many of codes and scales, got {codes.shape[0]} and {scales.shape[0]}")
+    return cp, ldc, sp, lds
+
+
+def moe_act(y13, h, pair_slot=None, stream=None):
+    """h[p] = silu(gate) * up of y13's rows [gate | up], for pairs with a slot (see lora_moe_act)."""
+    import torch
+    P, inter = int(h.shape[0]), int(h.shape[1])
+    yp, ldy = _rows(y13, 2 * inter, "y13")
+    if y13.shape[0] != P:
+        raise ValueError(f"moe_act: y13 has {y13.shape[0]} rows, h {P}")
+    hp, ldh = _rows(h, inter, "h")
+    check(lora_moe_act(yp, ldy, _dt(y13), _vec(pair_slot, P, "pair_slot", torch.int32), P, inter, hp, ldh, _dt(h),
+                       stream), "lora_moe_act")
+    return h
+
+
+def moe_act_mx4(y13, codes, scales, pair_slot=None, stream=None):
+    """moe_act into bf16, then mx4_quantize, in one pass (see lora_moe_act_mx)."""
+    import torch
+    P, inter = int(y13.shape[0]), int(y13.shape[1]) // 2
+    yp, ldy = _rows(y13, 2 * inter, "y13")
+    cp, ldc, sp, lds = _mx_ptrs(codes, scales, P, inter)
+    check(lora_moe_act_mx(yp, ldy, _dt(y13), _vec(pair_slot, P, "pair_slot", torch.int32), P, inter, cp, ldc, sp, lds,
+                          stream), "lora_moe_act_mx")
+    return codes, scales
+
+
+def moe_combine(y, topk_w, out, pair_slot=None, accumulate: bool = False, stream=None):
+    """out[t] (+)= sum_k topk_w[t, k] * y[t * topk + k] over the pairs with a slot (see lora_moe_combine)."""
+    import torch
+    T, topk, n = int(topk_w.shape[0]), int(topk_w.shape[1]), int(out.shape[1])
+    yp, ldy = _rows(y, n, "y")
+    op, ldo = _rows(out, n, "out")
+    if y.shape[0] != T * topk or out.shape[0] != T:
+        raise ValueError(f"moe_combine: {T} tokens of {topk} choices need {T * topk} rows of y and {T} of out, got "
+                         f"{y.shape[0]} and {out.shape[0]}")
+    check(lora_moe_combine(yp, ldy, _dt(y), _vec(topk_w, T * topk, "topk_w", torch.float32),
+                           _vec(pair_slot, T * topk, "pair_slot", torch.int32), T, topk, n, op, ldo, _dt(out),
+                           accumulate, stream), "lora_moe_combine")
+    return out

@@ -260,6 +260,25 @@ cudaError_t launch_moe_pair_slots(const int32_t *token_slot, const int32_t *topk
                                   cudaStream_t st);
 cudaError_t launch_embed_shrink(const lora_layer_desc &d, const MetaView &mv, const int32_t *token_slot,
                                 const int32_t *token_id, float *buf, cudaStream_t st);
+// The mixture-of-experts layer around its LoRA: products (moe_product.cu), the
+// 4-bit format (mx.cu), router, activation and weighted sum (moe_layer.cu).
+cudaError_t launch_moe_route(const void *logits, int64_t ldl, int dtype, int T, int E, int topk, int score, int renorm,
+                             float scale, const int32_t *expert_map, int local, int32_t *ids, float *w,
+                             int32_t *pair_slot, cudaStream_t st);
+cudaError_t launch_moe_product(const lora_expert_desc &d, const MetaView &mv, const void *x, int64_t ldx,
+                               const uint8_t *x_scale, int64_t ld_xs, void *y, int64_t ldy, int y_dtype,
+                               cudaStream_t st);
+cudaError_t launch_mx_quantize(const void *x, int64_t ldx, int x_dtype, int64_t rows, int cols, uint8_t *codes,
+                               int64_t ldc, uint8_t *scales, int64_t lds, cudaStream_t st);
+cudaError_t launch_mx_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t lds, int64_t rows,
+                                 int cols, void *y, int64_t ldy, int y_dtype, cudaStream_t st);
+cudaError_t launch_moe_act(const void *y13, int64_t ldy, int y_dtype, const int32_t *pair_slot, int P, int inter,
+                           void *h, int64_t ldh, int h_dtype, cudaStream_t st);
+cudaError_t launch_moe_act_mx(const void *y13, int64_t ldy, int y_dtype, const int32_t *pair_slot, int P, int inter,
+                              uint8_t *codes, int64_t ldc, uint8_t *scales, int64_t lds, cudaStream_t st);
+cudaError_t launch_moe_combine(const void *y, int64_t ldy, int y_dtype, const float *w, const int32_t *pair_slot, int T,
+                               int topk, int n, void *out, int64_t ldo, int out_dtype, int accumulate,
+                               cudaStream_t st);
 // SGMV family (sgmv.cu, tcgen05). part: split partials, sgmv_workspace_bytes() bytes.
 bool sgmv_supported();
 // The pipelines' bounded wait, run against a barrier nothing arms (see lora_probe_bounded_wait).

@@ -136,6 +136,39 @@ ra::MetaView view_of(const lora_meta *m) {
   return v;
 }
 
+// ---- the mixture-of-experts layer around its LoRA
+
+bool is_float(int dtype) { return dtype == LORA_F32 || dtype == LORA_BF16; }
+bool misaligned(const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+
+// Codes and scale bytes of rows of `cols` elements.
+int check_codes(int32_t cols, const uint8_t *codes, int64_t ld_codes, const uint8_t *scales, int64_t ld_scales) {
+  if (codes == nullptr || scales == nullptr) return LORA_EINVAL;
+  if (ld_codes < cols / 2 || ld_scales < cols / LORA_MX_BLOCK) return LORA_EINVAL;
+  if (!aligned16(codes) || !aligned16(scales) || ld_codes % 16 != 0 || ld_scales % 16 != 0) return LORA_EALIGN;
+  return LORA_OK;
+}
+
+int check_mx(const void *m, int64_t ld, int32_t dtype, int64_t rows, int32_t cols, const uint8_t *codes,
+             int64_t ld_codes, const uint8_t *scales, int64_t ld_scales) {
+  if (!is_float(dtype) || cols < LORA_MX_BLOCK || cols % LORA_MX_BLOCK != 0) return LORA_EINVAL;
+  if (rows < 0) return LORA_ERANGE;
+  if (rows == 0) return LORA_OK;
+  if (m == nullptr || ld < cols) return LORA_EINVAL;
+  if (!aligned16(m) || (ld * (int64_t)elem_size(dtype)) % 16 != 0) return LORA_EALIGN;
+  return check_codes(cols, codes, ld_codes, scales, ld_scales);
+}
+
+int check_act(const void *y13, int64_t ldy, int32_t y_dtype, const int32_t *pair_slot, int32_t num_pairs,
+              int32_t inter, int32_t multiple) {
+  if (!is_float(y_dtype) || inter < multiple || inter % multiple != 0 || inter > INT32_MAX / 2) return LORA_EINVAL;
+  if (num_pairs < 0 || num_pairs > LORA_MAX_TOKENS) return LORA_ERANGE;
+  if (num_pairs == 0) return LORA_OK;
+  if (y13 == nullptr || ldy < 2 * (int64_t)inter) return LORA_EINVAL;
+  if (!aligned16(y13) || (ldy * (int64_t)elem_size(y_dtype)) % 16 != 0 || misaligned(pair_slot, 4)) return LORA_EALIGN;
+  return LORA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -375,6 +408,119 @@ int lora_moe_pair_slots(const int32_t *token_slot, const int32_t *topk_ids, int3
     return LORA_EALIGN;
   return cuda_status(ra::launch_moe_pair_slots(token_slot, topk_ids, num_tokens, topk, num_loras, num_experts,
                                                local_experts, expert_map, pair_slot, (cudaStream_t)stream));
+}
+
+int lora_moe_route(const void *logits, int64_t ld_logits, int32_t dtype, int32_t num_tokens, int32_t num_experts,
+                   int32_t topk, int32_t score, int32_t renormalize, float scale, const int32_t *expert_map,
+                   int32_t local_experts, int32_t *topk_ids, float *topk_w, int32_t *pair_slot, lora_stream_t stream) {
+  clear_stale_error();
+  if (!is_float(dtype) || (score != LORA_SCORE_SOFTMAX && score != LORA_SCORE_SIGMOID)) return LORA_EINVAL;
+  if (num_experts < 1 || num_experts > LORA_MAX_EXPERTS) return LORA_ERANGE;
+  if (topk < 1 || topk > std::min<int32_t>(num_experts, LORA_MAX_ROUTE_TOPK)) return LORA_ERANGE;
+  if (num_tokens < 0 || (int64_t)num_tokens * topk > LORA_MAX_TOKENS) return LORA_ERANGE;
+  if (pair_slot != nullptr && (local_experts < 1 || local_experts > num_experts)) return LORA_ERANGE;
+  if (num_tokens == 0) return LORA_OK;
+  if (logits == nullptr || topk_ids == nullptr || topk_w == nullptr) return LORA_EINVAL;
+  if (ld_logits < num_experts) return LORA_EINVAL;
+  if (misaligned(logits, elem_size(dtype)) || misaligned(topk_ids, 4) || misaligned(topk_w, 4) ||
+      misaligned(pair_slot, 4) || misaligned(expert_map, 4))
+    return LORA_EALIGN;
+  return cuda_status(ra::launch_moe_route(logits, ld_logits, dtype, num_tokens, num_experts, topk, score,
+                                          renormalize != 0, scale, expert_map, local_experts, topk_ids, topk_w,
+                                          pair_slot, (cudaStream_t)stream));
+}
+
+int lora_moe_product(const lora_expert_desc *desc, const lora_meta *meta, const void *x, int64_t ldx,
+                     const uint8_t *x_scale, int64_t ld_xscale, void *y, int64_t ldy, int32_t y_dtype,
+                     lora_stream_t stream) {
+  clear_stale_error();
+  if (desc == nullptr) return LORA_EINVAL;
+  const bool mx = desc->dtype == LORA_MXFP4;
+  if (!mx && !is_float(desc->dtype)) return LORA_EINVAL;
+  if (desc->d_in < 8 || desc->d_in % (mx ? LORA_MX_BLOCK : 8) != 0 || desc->d_out < 8 || desc->d_out % 8 != 0 ||
+      desc->x_row_div < 0 || desc->W == nullptr)
+    return LORA_EINVAL;
+  if (desc->num_experts < 1 || desc->num_experts >= LORA_MAX_NUM_SLOTS) return LORA_ERANGE;
+  if (!aligned16(desc->W)) return LORA_EALIGN;
+  const int64_t blocks = desc->d_in / LORA_MX_BLOCK;
+  if (mx) {
+    if (desc->W_scale == nullptr || desc->ld_scale < blocks) return LORA_EINVAL;
+    if (!aligned16(desc->W_scale) || desc->ld_scale % 16 != 0) return LORA_EALIGN;
+  }
+  int st = check_meta(meta);
+  if (st != LORA_OK) return st;
+  if (meta->num_slots != desc->num_experts + 1) return LORA_EINVAL;
+  if (!is_float(y_dtype)) return LORA_EINVAL;
+  if (desc->dtype == LORA_F32 && y_dtype != LORA_F32) return LORA_EUNSUPPORTED;
+  if (meta->num_tokens == 0) return LORA_OK;
+  if (x == nullptr || y == nullptr || ldx < desc->d_in || ldy < desc->d_out) return LORA_EINVAL;
+  if (mx) {
+    if (x_scale == nullptr || ld_xscale < blocks) return LORA_EINVAL;
+    if (!aligned16(x_scale) || ld_xscale % 16 != 0 || ldx % 32 != 0) return LORA_EALIGN;
+  } else if ((ldx * (int64_t)elem_size(desc->dtype)) % 16 != 0) {
+    return LORA_EALIGN;
+  }
+  if (!aligned16(x) || !aligned16(y) || (ldy * (int64_t)elem_size(y_dtype)) % 16 != 0) return LORA_EALIGN;
+  return cuda_status(ra::launch_moe_product(*desc, view_of(meta), x, ldx, x_scale, ld_xscale, y, ldy, y_dtype,
+                                            (cudaStream_t)stream));
+}
+
+int lora_mx_quantize(const void *x, int64_t ldx, int32_t x_dtype, int64_t rows, int32_t cols, uint8_t *codes,
+                     int64_t ld_codes, uint8_t *scales, int64_t ld_scales, lora_stream_t stream) {
+  clear_stale_error();
+  const int st = check_mx(x, ldx, x_dtype, rows, cols, codes, ld_codes, scales, ld_scales);
+  if (st != LORA_OK || rows == 0) return st;
+  return cuda_status(ra::launch_mx_quantize(x, ldx, x_dtype, rows, cols, codes, ld_codes, scales, ld_scales,
+                                            (cudaStream_t)stream));
+}
+
+int lora_mx_dequantize(const uint8_t *codes, int64_t ld_codes, const uint8_t *scales, int64_t ld_scales, int64_t rows,
+                       int32_t cols, void *y, int64_t ldy, int32_t y_dtype, lora_stream_t stream) {
+  clear_stale_error();
+  const int st = check_mx(y, ldy, y_dtype, rows, cols, codes, ld_codes, scales, ld_scales);
+  if (st != LORA_OK || rows == 0) return st;
+  return cuda_status(ra::launch_mx_dequantize(codes, ld_codes, scales, ld_scales, rows, cols, y, ldy, y_dtype,
+                                              (cudaStream_t)stream));
+}
+
+int lora_moe_act(const void *y13, int64_t ldy, int32_t y_dtype, const int32_t *pair_slot, int32_t num_pairs,
+                 int32_t inter, void *h, int64_t ldh, int32_t h_dtype, lora_stream_t stream) {
+  clear_stale_error();
+  const int st = check_act(y13, ldy, y_dtype, pair_slot, num_pairs, inter, 8);
+  if (st != LORA_OK) return st;
+  if (!is_float(h_dtype)) return LORA_EINVAL;
+  if (num_pairs == 0) return LORA_OK;
+  if (h == nullptr || ldh < inter) return LORA_EINVAL;
+  if (!aligned16(h) || (ldh * (int64_t)elem_size(h_dtype)) % 16 != 0) return LORA_EALIGN;
+  return cuda_status(ra::launch_moe_act(y13, ldy, y_dtype, pair_slot, num_pairs, inter, h, ldh, h_dtype,
+                                        (cudaStream_t)stream));
+}
+
+int lora_moe_act_mx(const void *y13, int64_t ldy, int32_t y_dtype, const int32_t *pair_slot, int32_t num_pairs,
+                    int32_t inter, uint8_t *codes, int64_t ld_codes, uint8_t *scales, int64_t ld_scales,
+                    lora_stream_t stream) {
+  clear_stale_error();
+  int st = check_act(y13, ldy, y_dtype, pair_slot, num_pairs, inter, LORA_MX_BLOCK);
+  if (st != LORA_OK || num_pairs == 0) return st;
+  st = check_codes(inter, codes, ld_codes, scales, ld_scales);
+  if (st != LORA_OK) return st;
+  return cuda_status(ra::launch_moe_act_mx(y13, ldy, y_dtype, pair_slot, num_pairs, inter, codes, ld_codes, scales,
+                                           ld_scales, (cudaStream_t)stream));
+}
+
+int lora_moe_combine(const void *y, int64_t ldy, int32_t y_dtype, const float *topk_w, const int32_t *pair_slot,
+                     int32_t num_tokens, int32_t topk, int32_t n, void *out, int64_t ldo, int32_t out_dtype,
+                     int32_t accumulate, lora_stream_t stream) {
+  clear_stale_error();
+  if (!is_float(y_dtype) || !is_float(out_dtype) || n < 8 || n % 8 != 0) return LORA_EINVAL;
+  if (topk < 1 || topk > 64 || num_tokens < 0 || (int64_t)num_tokens * topk > LORA_MAX_TOKENS) return LORA_ERANGE;
+  if (num_tokens == 0) return LORA_OK;
+  if (y == nullptr || topk_w == nullptr || out == nullptr || ldy < n || ldo < n) return LORA_EINVAL;
+  if (!aligned16(y) || !aligned16(out) || (ldy * (int64_t)elem_size(y_dtype)) % 16 != 0 ||
+      (ldo * (int64_t)elem_size(out_dtype)) % 16 != 0 || misaligned(topk_w, 4) || misaligned(pair_slot, 4))
+    return LORA_EALIGN;
+  return cuda_status(ra::launch_moe_combine(y, ldy, y_dtype, topk_w, pair_slot, num_tokens, topk, n, out, ldo,
+                                            out_dtype, accumulate != 0, (cudaStream_t)stream));
 }
 
 }  // extern "C"

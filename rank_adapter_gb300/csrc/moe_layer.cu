@@ -1,0 +1,308 @@
+// The parts of a mixture-of-experts layer around its products: the router
+// (lora_moe_route), the gated activation between w13 and w2 (lora_moe_act,
+// lora_moe_act_mx) and the weighted sum over a token's choices
+// (lora_moe_combine). Pairs are token-major, p = t * topk + k.
+#include "mx.cuh"
+
+namespace ra {
+namespace {
+
+// ------------------------------------------------------------------ router
+//
+// One warp a token: lane l holds logits l, l + 32, ... in registers. A round
+// finds the warp's largest key (redux.sync) and among the lanes that hold it
+// the lowest expert; topk rounds choose topk experts, so a row is read once
+// and nothing is sorted that is not asked for. Lane k keeps choice k and the
+// weights need one or two warp sums.
+
+constexpr int kRouteWarps = 4;
+
+struct RouteArgs {
+  const void *logits;
+  int64_t ldl;
+  int32_t *ids;
+  float *w;
+  const int32_t *expert_map;
+  int32_t *pair_slot;
+  int T, E, topk, local;
+  int sigmoid, renorm;
+  float scale;
+};
+
+// Order-preserving key of a logit; 0 is below every key. NaN counts as
+// -infinity, +infinity as the largest finite number (so that a row's weights
+// stay numbers), -0 as 0.
+__device__ __forceinline__ uint32_t route_key(float v) {
+  if (isnan(v)) v = -INFINITY;
+  const uint32_t u = __float_as_uint(fminf(v, 3.402823466e38f) + 0.f);
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float route_value(uint32_t key) {
+  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(RouteArgs a) {
+  // The next kernel may read pair_slot before its wait (lora_prepare_meta), so
+  // this one releases it only by completing.
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  constexpr uint32_t kAll = 0xffffffffu;
+  const uint32_t kNegInf = route_key(-INFINITY);
+  for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5); t < a.T;
+       t += (int64_t)gridDim.x * kRouteWarps) {
+    const T *row = static_cast<const T *>(a.logits) + t * a.ldl;
+    uint32_t key[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = lane + 32 * i;
+      key[i] = e < a.E ? route_key(Elem<T>::to_f(row[e])) : 0u;
+    }
+    float total = 0.f;  // softmax without renormalisation: the sum over all experts
+    if (!a.sigmoid && !a.renorm) {
+      uint32_t m = key[0];
+#pragma unroll
+      for (int i = 1; i < NV; ++i) m = max(m, key[i]);
+      const float top = route_value(__reduce_max_sync(kAll, m));
+      if (top != -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (key[i] > kNegInf) total += expf(route_value(key[i]) - top);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+    }
+    uint32_t mine = 0;  // key of choice `lane`
+    int id = 0;
+    float top = 0.f;
+    for (int k = 0; k < a.topk; ++k) {
+      uint32_t m = key[0];
+#pragma unroll
+      for (int i = 1; i < NV; ++i) m = max(m, key[i]);
+      const uint32_t best = __reduce_max_sync(kAll, m);
+      int e = 0x7fffffff;
+#pragma unroll
+      for (int i = NV - 1; i >= 0; --i)
+        if (key[i] == best) e = lane + 32 * i;
+      const int win = (int)__reduce_min_sync(kAll, (uint32_t)e);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (lane + 32 * i == win) key[i] = 0u;
+      if (k == 0) top = route_value(best);
+      if (lane == k) {
+        mine = best;
+        id = win;
+      }
+    }
+    const bool chosen = lane < a.topk, live = chosen && mine > kNegInf;
+    float w = 0.f;
+    if (live) {
+      const float v = route_value(mine);
+      w = a.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top);
+    }
+    if (a.renorm) {
+      total = w;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+    }
+    if ((a.renorm || !a.sigmoid) && total > 0.f) w /= total;
+    if (!chosen) continue;
+    const int64_t p = t * a.topk + lane;
+    a.ids[p] = id;
+    a.w[p] = w * a.scale;
+    if (a.pair_slot != nullptr) {
+      const int el = a.expert_map != nullptr ? a.expert_map[id] : id;
+      a.pair_slot[p] = el >= a.local ? -1 : (el < 0 || !live) ? 0 : 1 + el;
+    }
+  }
+}
+
+template <typename T>
+cudaError_t route_launch(const RouteArgs &a, cudaStream_t st) {
+  const int nv = (a.E + 31) / 32;
+  void (*k)(RouteArgs) = nv <= 1 ? moe_route_kernel<T, 1> : nv <= 2 ? moe_route_kernel<T, 2>
+                       : nv <= 4 ? moe_route_kernel<T, 4> : nv <= 8 ? moe_route_kernel<T, 8>
+                       : nv <= 16 ? moe_route_kernel<T, 16> : moe_route_kernel<T, 32>;
+  const int blocks = (int)std::min<int64_t>(((int64_t)a.T + kRouteWarps - 1) / kRouteWarps, 152 * 64);
+  return launch_pdl(k, dim3((unsigned)blocks), dim3(kRouteWarps * 32), 0, st, 1u, a);
+}
+
+// ------------------------------------------------------------------ activation
+//
+// h = silu(gate) * up over rows of [gate | up], eight elements a thread;
+// rows of pairs without a local expert are neither read nor written.
+
+constexpr int kThreads = 256;
+
+struct ActArgs {
+  const void *y13;
+  int64_t ldy;
+  const int32_t *pair_slot;
+  void *h;         // bf16 / f32 rows, or the codes of the 4-bit form
+  int64_t ldh;     // elements; bytes of a row of codes
+  uint8_t *scales;
+  int64_t lds;
+  int P, inter;
+};
+
+__device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
+
+template <typename TY>
+__device__ __forceinline__ void act8(const TY *row, int inter, int c, float (&v)[8]) {
+  float u[8];
+  load8_f32(row + c * 8, v);
+  load8_f32(row + inter + c * 8, u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = silu(v[i]) * u[i];
+}
+
+template <typename TY, typename TH>
+__global__ void __launch_bounds__(kThreads) moe_act_kernel(ActArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int chunks = a.inter / 8, c = blockIdx.x * blockDim.x + threadIdx.x;
+  if (c >= chunks) return;
+  for (int64_t p = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; p < a.P; p += (int64_t)gridDim.y * blockDim.y) {
+    if (a.pair_slot != nullptr && a.pair_slot[p] <= 0) continue;
+    float v[8];
+    act8(static_cast<const TY *>(a.y13) + p * a.ldy, a.inter, c, v);
+    store8(static_cast<TH *>(a.h) + p * a.ldh + (int64_t)c * 8, v);
+  }
+}
+
+// The same into the 4-bit format. The activation is rounded to bf16 first, so
+// that the result is bitwise that of lora_moe_act into bf16 and
+// lora_mx_quantize after it.
+template <typename TY>
+__global__ void __launch_bounds__(kThreads) moe_act_mx_kernel(ActArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int chunks = a.inter / 8, c = blockIdx.x * blockDim.x + threadIdx.x;
+  for (int64_t p0 = (int64_t)blockIdx.y * blockDim.y; p0 < a.P; p0 += (int64_t)gridDim.y * blockDim.y) {
+    const int64_t p = p0 + threadIdx.y;
+    // The four lanes of a block of 32 are in one row and in range together.
+    const bool in = p < a.P && c < chunks && (a.pair_slot == nullptr || a.pair_slot[p] > 0);
+    float v[8] = {};
+    if (in) {
+      act8(static_cast<const TY *>(a.y13) + p * a.ldy, a.inter, c, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(__float2bfloat16_rn(v[i]));
+    }
+    uint32_t byte;
+    const uint32_t q = mx_quantize8(v, byte);
+    if (in) {
+      *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.h) + p * a.ldh + (int64_t)c * 4) = q;
+      if ((c & 3) == 0) a.scales[p * a.lds + (c >> 2)] = (uint8_t)byte;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ weighted sum
+//
+// out[t] = (out[t] or 0) + sum_k w[t, k] * y[t * topk + k], in fp32 in the
+// order of k and rounded once. A thread owns eight columns of a token; the
+// rows of up to kAhead choices are requested before the first is used.
+
+struct CombineArgs {
+  const void *y;
+  int64_t ldy;
+  const float *w;
+  const int32_t *pair_slot;
+  void *out;
+  int64_t ldo;
+  int T, topk, n;
+  int accumulate;
+};
+
+template <typename TY, typename TO>
+__global__ void __launch_bounds__(kThreads) moe_combine_kernel(CombineArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int kAhead = sizeof(TY) == 2 ? 8 : 4;
+  const int chunks = a.n / 8, c = blockIdx.x * blockDim.x + threadIdx.x;
+  if (c >= chunks) return;
+  for (int64_t t = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; t < a.T; t += (int64_t)gridDim.y * blockDim.y) {
+    TO *o = static_cast<TO *>(a.out) + t * a.ldo + (int64_t)c * 8;
+    float acc[8] = {};
+    if (a.accumulate) load8_rw(o, acc);
+    const float *w = a.w + t * a.topk;
+    const int32_t *slot = a.pair_slot != nullptr ? a.pair_slot + t * a.topk : nullptr;
+    const TY *y = static_cast<const TY *>(a.y) + t * a.topk * a.ldy + (int64_t)c * 8;
+    for (int k0 = 0; k0 < a.topk; k0 += kAhead) {
+      float v[kAhead][8], wk[kAhead];
+      bool live[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int k = k0 + i;
+        live[i] = k < a.topk && (slot == nullptr || slot[k] > 0);
+        if (live[i]) {
+          wk[i] = w[k];
+          load8_f32(y + k * a.ldy, v[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (!live[i]) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] = fmaf(wk[i], v[i][j], acc[j]);
+      }
+    }
+    store8(o, acc);
+  }
+}
+
+// CTA shape for rows of `chunks` eight-element chunks: threads along a row (a
+// power of two of at least 4) by rows.
+struct Launch {
+  dim3 grid, block;
+};
+Launch shape_of(int64_t rows, int chunks, int threads) {
+  int tx = 4;
+  while (tx < threads && tx < chunks) tx *= 2;
+  const int ty = threads / tx;
+  return {dim3((unsigned)((chunks + tx - 1) / tx), (unsigned)std::min<int64_t>((rows + ty - 1) / ty, 65535)),
+          dim3((unsigned)tx, (unsigned)ty)};
+}
+
+}  // namespace
+
+cudaError_t launch_moe_route(const void *logits, int64_t ldl, int dtype, int T, int E, int topk, int score, int renorm,
+                             float scale, const int32_t *expert_map, int local, int32_t *ids, float *w,
+                             int32_t *pair_slot, cudaStream_t st) {
+  RouteArgs a{logits, ldl, ids, w, expert_map, pair_slot, T, E, topk, local, score == LORA_SCORE_SIGMOID, renorm, scale};
+  return dtype == LORA_BF16 ? route_launch<__nv_bfloat16>(a, st) : route_launch<float>(a, st);
+}
+
+cudaError_t launch_moe_act(const void *y13, int64_t ldy, int y_dtype, const int32_t *pair_slot, int P, int inter,
+                           void *h, int64_t ldh, int h_dtype, cudaStream_t st) {
+  const ActArgs a{y13, ldy, pair_slot, h, ldh, nullptr, 0, P, inter};
+  const Launch l = shape_of(P, inter / 8, kThreads);
+  void (*k)(ActArgs) =
+      y_dtype == LORA_BF16
+          ? (h_dtype == LORA_BF16 ? moe_act_kernel<__nv_bfloat16, __nv_bfloat16> : moe_act_kernel<__nv_bfloat16, float>)
+          : (h_dtype == LORA_BF16 ? moe_act_kernel<float, __nv_bfloat16> : moe_act_kernel<float, float>);
+  return launch_pdl(k, l.grid, l.block, 0, st, 1u, a);
+}
+
+cudaError_t launch_moe_act_mx(const void *y13, int64_t ldy, int y_dtype, const int32_t *pair_slot, int P, int inter,
+                              uint8_t *codes, int64_t ldc, uint8_t *scales, int64_t lds, cudaStream_t st) {
+  const ActArgs a{y13, ldy, pair_slot, codes, ldc, scales, lds, P, inter};
+  const Launch l = shape_of(P, inter / 8, kThreads);
+  return launch_pdl(y_dtype == LORA_BF16 ? moe_act_mx_kernel<__nv_bfloat16> : moe_act_mx_kernel<float>, l.grid, l.block,
+                    0, st, 1u, a);
+}
+
+cudaError_t launch_moe_combine(const void *y, int64_t ldy, int y_dtype, const float *w, const int32_t *pair_slot, int T,
+                               int topk, int n, void *out, int64_t ldo, int out_dtype, int accumulate,
+                               cudaStream_t st) {
+  const CombineArgs a{y, ldy, w, pair_slot, out, ldo, T, topk, n, accumulate};
+  const Launch l = shape_of(T, n / 8, kThreads);
+  void (*k)(CombineArgs) = y_dtype == LORA_BF16
+                               ? (out_dtype == LORA_BF16 ? moe_combine_kernel<__nv_bfloat16, __nv_bfloat16>
+                                                         : moe_combine_kernel<__nv_bfloat16, float>)
+                               : (out_dtype == LORA_BF16 ? moe_combine_kernel<float, __nv_bfloat16>
+                                                         : moe_combine_kernel<float, float>);
+  return launch_pdl(k, l.grid, l.block, 0, st, 1u, a);
+}
+
+}  // namespace ra

@@ -1,0 +1,132 @@
+"""The mixture-of-experts operators refuse bad arguments on the host, before any launch (no GPU needed)."""
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = 0x10000
+
+
+@pytest.fixture(scope="module")
+def ra():
+    import __graft_entry__
+    __graft_entry__._load_build_lib().build()
+    import rank_adapter_gb300
+    return rank_adapter_gb300
+
+
+def test_constants_match_the_header(ra):
+    src = open(os.path.join(ROOT, "include", "lora.h")).read()
+    for name in ("LORA_MAX_EXPERTS", "LORA_MAX_ROUTE_TOPK", "LORA_MX_BLOCK"):
+        assert int(re.search(rf"#define {name} (\d+)", src).group(1)) == getattr(ra, name)
+    assert re.search(rf"LORA_MXFP4 = {ra.LORA_MXFP4}\b", src)
+    assert re.search(rf"LORA_SCORE_SOFTMAX = {ra.LORA_SCORE_SOFTMAX}, LORA_SCORE_SIGMOID = {ra.LORA_SCORE_SIGMOID}\b", src)
+
+
+def test_route(ra):
+    def f(logits=P, ld=64, dt=ra.LORA_F32, T=5, E=64, topk=4, score=0, emap=0, local=64, ids=P, w=P, slot=0):
+        return ra.lora_moe_route(logits, ld, dt, T, E, topk, score, True, 1.0, emap, local, ids, w, slot, 0)
+    assert f(T=0, logits=0, ids=0, w=0) == ra.LORA_OK
+    for kw in (dict(dt=ra.LORA_MXFP4), dict(score=2), dict(logits=0), dict(ids=0), dict(w=0), dict(ld=63)):
+        assert f(**kw) == ra.LORA_EINVAL, kw
+    for kw in (dict(E=0), dict(E=1025, ld=2000), dict(topk=0), dict(topk=33), dict(E=3, topk=4), dict(T=-1),
+               dict(T=1 << 24), dict(slot=P, local=0), dict(slot=P, local=65)):
+        assert f(**kw) == ra.LORA_ERANGE, kw
+    for kw in (dict(logits=P + 2), dict(ids=P + 2), dict(w=P + 1), dict(slot=P + 2), dict(emap=P + 3)):
+        assert f(**kw) == ra.LORA_EALIGN, kw
+
+
+def _meta(ra, T=8, S=5):
+    m = ra.Meta()
+    m.token_slot, m.num_tokens, m.num_slots = 0x1000, T, S
+    m.sorted_rows = m.seg_slot = m.seg_count = m.seg_start = 0x2000
+    m.num_segs, m.no_lora, m.status = 0x3000, 0x3004, 0x3008
+    m.tiles, m.tiles_bytes = 0x4000, ra.lora_meta_tiles_bytes(S)
+    return m
+
+
+def test_product(ra):
+    def f(dt=ra.LORA_BF16, K=64, N=32, E=4, W=P, ws=0, lws=0, div=1, T=8, S=5, x=P, ldx=64, xs=0, lxs=0, y=P, ldy=32,
+          ydt=ra.LORA_BF16, meta=True):
+        d = ra.ExpertDesc()
+        d.dtype, d.d_in, d.d_out, d.num_experts, d.W, d.W_scale, d.ld_scale, d.x_row_div = dt, K, N, E, W, ws or None, lws, div
+        return ra.lora_moe_product(d, _meta(ra, T, S), x, ldx, xs, lxs, y, ldy, ydt, 0)
+    mx = dict(dt=ra.LORA_MXFP4, ws=P, lws=16, xs=P, lxs=16)
+    assert f(T=0, x=0, y=0) == ra.LORA_OK and f(**{**mx, "T": 0}) == ra.LORA_OK
+    for kw in (dict(dt=9), dict(K=0), dict(K=12), dict(N=0), dict(N=12), dict(div=-1), dict(W=0), dict(S=6), dict(x=0),
+               dict(y=0), dict(ldx=56), dict(ldy=24), dict(ydt=ra.LORA_MXFP4), {**mx, "ws": 0}, {**mx, "xs": 0},
+               {**mx, "K": 40, "ldx": 64}, {**mx, "lws": 0}, {**mx, "lxs": 0}):
+        assert f(**kw) == ra.LORA_EINVAL, kw
+    for kw in (dict(E=0, S=1), dict(E=1024, S=1025), dict(T=-1)):
+        assert f(**kw) == ra.LORA_ERANGE, kw
+    for kw in (dict(W=P + 8), dict(x=P + 8), dict(y=P + 2), dict(ldx=68), dict(ldy=36), {**mx, "ws": P + 8},
+               {**mx, "xs": P + 4}, {**mx, "lws": 24}, {**mx, "lxs": 20}, {**mx, "ldx": 80}):
+        assert f(**kw) == ra.LORA_EALIGN, kw
+    assert f(dt=ra.LORA_F32) == ra.LORA_EUNSUPPORTED
+
+
+def test_mx(ra):
+    def f(x=P, ldx=64, dt=ra.LORA_BF16, rows=3, cols=64, c=P, ldc=32, s=P, lds=16):
+        a = ra.lora_mx_quantize(x, ldx, dt, rows, cols, c, ldc, s, lds, 0)
+        assert a == ra.lora_mx_dequantize(c, ldc, s, lds, rows, cols, x, ldx, dt, 0)
+        return a
+    assert f(rows=0, x=0, c=0, s=0) == ra.LORA_OK
+    for kw in (dict(dt=ra.LORA_MXFP4), dict(cols=0), dict(cols=48), dict(x=0), dict(c=0), dict(s=0), dict(ldx=32),
+               dict(ldc=16), dict(lds=0)):
+        assert f(**kw) == ra.LORA_EINVAL, kw
+    assert f(rows=-1) == ra.LORA_ERANGE
+    for kw in (dict(x=P + 2), dict(ldx=68), dict(c=P + 4), dict(ldc=40), dict(s=P + 1), dict(lds=24)):
+        assert f(**kw) == ra.LORA_EALIGN, kw
+
+
+def test_act(ra):
+    def f(y=P, ldy=128, ydt=ra.LORA_BF16, slot=P, n=4, inter=64, h=P, ldh=64, hdt=ra.LORA_BF16):
+        return ra.lora_moe_act(y, ldy, ydt, slot, n, inter, h, ldh, hdt, 0)
+    assert f(n=0, y=0, h=0) == ra.LORA_OK
+    for kw in (dict(ydt=5), dict(hdt=ra.LORA_MXFP4), dict(inter=0), dict(inter=12), dict(y=0), dict(h=0), dict(ldy=120),
+               dict(ldh=56)):
+        assert f(**kw) == ra.LORA_EINVAL, kw
+    assert f(n=-1) == ra.LORA_ERANGE and f(n=(1 << 24) + 1) == ra.LORA_ERANGE
+    for kw in (dict(y=P + 4), dict(h=P + 8), dict(slot=P + 2), dict(ldy=132), dict(ldh=68)):
+        assert f(**kw) == ra.LORA_EALIGN, kw
+
+    def g(y=P, inter=64, n=4, c=P, ldc=32, s=P, lds=16):
+        return ra.lora_moe_act_mx(y, 128, ra.LORA_BF16, 0, n, inter, c, ldc, s, lds, 0)
+    assert g(n=0, y=0, c=0, s=0) == ra.LORA_OK
+    for kw in (dict(inter=40), dict(y=0), dict(c=0), dict(s=0), dict(ldc=16), dict(lds=0)):
+        assert g(**kw) == ra.LORA_EINVAL, kw
+    for kw in (dict(y=P + 8), dict(c=P + 8), dict(ldc=40), dict(s=P + 2), dict(lds=20)):
+        assert g(**kw) == ra.LORA_EALIGN, kw
+
+
+def test_combine(ra):
+    def f(y=P, ldy=64, ydt=ra.LORA_BF16, w=P, slot=P, T=3, topk=2, n=64, out=P, ldo=64, odt=ra.LORA_BF16):
+        return ra.lora_moe_combine(y, ldy, ydt, w, slot, T, topk, n, out, ldo, odt, False, 0)
+    assert f(T=0, y=0, w=0, out=0) == ra.LORA_OK
+    for kw in (dict(ydt=ra.LORA_MXFP4), dict(odt=7), dict(n=0), dict(n=12), dict(y=0), dict(w=0), dict(out=0),
+               dict(ldy=56), dict(ldo=56)):
+        assert f(**kw) == ra.LORA_EINVAL, kw
+    for kw in (dict(topk=0), dict(topk=65), dict(T=-1), dict(T=1 << 23, topk=4)):
+        assert f(**kw) == ra.LORA_ERANGE, kw
+    for kw in (dict(y=P + 2), dict(out=P + 8), dict(w=P + 2), dict(slot=P + 1), dict(ldy=68), dict(ldo=68)):
+        assert f(**kw) == ra.LORA_EALIGN, kw
+
+
+def test_binding_checks_shapes(ra):
+    import torch
+    z = torch.zeros
+    with pytest.raises(ValueError):
+        ra.ExpertWeights(z(2, 16, 32).transpose(1, 2))
+    with pytest.raises(ValueError):
+        ra.ExpertWeights(z(2, 16, 16, dtype=torch.uint8), z(2, 8, 16, dtype=torch.uint8))
+    with pytest.raises(TypeError):
+        ra.ExpertWeights(z(2, 16, 32, dtype=torch.float16))
+    with pytest.raises(ValueError):
+        ra.moe_combine(z(6, 16), z(2, 2), z(2, 16))
+    with pytest.raises(ValueError):
+        ra.moe_act(z(4, 32), z(3, 16))
+    with pytest.raises(ValueError):
+        ra.mx4_dequantize(z(3, 16, dtype=torch.uint8), z(3, 16, dtype=torch.uint8), z(4, 32))
+    with pytest.raises(ValueError):
+        ra.moe_route(z(4, 32).t(), 2)
