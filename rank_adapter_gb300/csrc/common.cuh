@@ -268,6 +268,9 @@ cudaError_t launch_moe_route(const void *logits, int64_t ldl, int dtype, int T, 
 cudaError_t launch_moe_product(const lora_expert_desc &d, const MetaView &mv, const void *x, int64_t ldx,
                                const uint8_t *x_scale, int64_t ld_xs, void *y, int64_t ldy, int y_dtype,
                                cudaStream_t st);
+cudaError_t launch_moe_product_tc(const lora_expert_desc &d, const MetaView &mv, const void *x, int64_t ldx,
+                                  const uint8_t *x_scale, int64_t ld_xs, void *y, int64_t ldy, int y_dtype,
+                                  cudaStream_t st);  // bf16 and 4-bit weights (moe_product_tc.cu)
 cudaError_t launch_mx_quantize(const void *x, int64_t ldx, int x_dtype, int64_t rows, int cols, uint8_t *codes,
                                int64_t ldc, uint8_t *scales, int64_t lds, cudaStream_t st);
 cudaError_t launch_mx_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t lds, int64_t rows,

@@ -1,8 +1,10 @@
 // The experts' own products (lora_moe_product): pairs grouped by local expert
 // through the token metadata, y[p] = x[p / x_row_div] . W[slot p - 1]^T.
+// fp32 weights (accuracy runs) go to a CUDA-core kernel, bf16 and 4-bit ones
+// to the tensor cores (moe_product_tc.cu).
 //
 // CUDA-core kernel: 64 rows by 64 outputs a CTA, fp32 sums.
-#include "mx.cuh"
+#include "common.cuh"
 
 namespace ra {
 namespace {
@@ -12,39 +14,13 @@ constexpr int kStep = 16;   // elements of d_in a step
 constexpr int kThreads = 256;
 
 struct ProductArgs {
-  const void *x, *W;
-  const uint8_t *x_scale, *W_scale;
-  int64_t ldx, ld_xs, ld_ws, ldy;
-  void *y;
+  const float *x, *W;
+  int64_t ldx, ldy;
+  float *y;
   const int32_t *work, *sorted_rows;
   int num_slots, K, N, x_div;
 };
 
-// Element k of row r of a matrix of the given type.
-struct RowsF32 {
-  const float *p;
-  int64_t ld;
-  __device__ RowsF32(const void *b, const uint8_t *, int64_t ld_, int64_t) : p(static_cast<const float *>(b)), ld(ld_) {}
-  __device__ float at(int64_t r, int k) const { return p[r * ld + k]; }
-};
-struct RowsBf16 {
-  const __nv_bfloat16 *p;
-  int64_t ld;
-  __device__ RowsBf16(const void *b, const uint8_t *, int64_t ld_, int64_t)
-      : p(static_cast<const __nv_bfloat16 *>(b)), ld(ld_) {}
-  __device__ float at(int64_t r, int k) const { return __bfloat162float(p[r * ld + k]); }
-};
-struct RowsMx {
-  const uint8_t *p, *s;
-  int64_t ld, lds;
-  __device__ RowsMx(const void *b, const uint8_t *s_, int64_t ld_, int64_t lds_)
-      : p(static_cast<const uint8_t *>(b)), s(s_), ld(ld_ / 2), lds(lds_) {}
-  __device__ float at(int64_t r, int k) const {
-    return mx_decode(p[r * ld + (k >> 1)] >> (4 * (k & 1)) & 15u) * mx_scale(s[r * lds + k / kMxBlock]);
-  }
-};
-
-template <typename Rows, typename TY>
 __global__ void __launch_bounds__(kThreads) moe_product_kernel(ProductArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -54,7 +30,6 @@ __global__ void __launch_bounds__(kThreads) moe_product_kernel(ProductArgs a) {
   const int32_t *ts = a.work + WorkLists::all_tile_start(S);
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   const int n0 = blockIdx.x * kTile;
-  const Rows X(a.x, a.x_scale, a.ldx, a.ld_xs);
   constexpr int kHalves = LORA_SGMV_TILE_M / kTile;
   for (int it = blockIdx.y; it < n_tiles * kHalves; it += gridDim.y) {
     const int tile = it / kHalves;
@@ -72,14 +47,13 @@ __global__ void __launch_bounds__(kThreads) moe_product_kernel(ProductArgs a) {
     __syncthreads();
     if (threadIdx.x < kTile) rows_s[threadIdx.x] = a.sorted_rows[rec[3] + first + min((int)threadIdx.x, rows - 1)];
     __syncthreads();
-    const Rows W(a.W, a.W_scale, a.K, a.ld_ws);
     float acc[4][4] = {};
     for (int k0 = 0; k0 < a.K; k0 += kStep) {
       for (int i = threadIdx.x; i < kTile * kStep; i += kThreads) {
         const int r = i / kStep, k = i % kStep;
         const bool in = k0 + k < a.K;
-        xs[k][r] = in ? X.at(rows_s[r] / a.x_div, k0 + k) : 0.f;
-        ws[k][r] = in && n0 + r < a.N ? W.at(w0 + n0 + r, k0 + k) : 0.f;
+        xs[k][r] = in ? a.x[(int64_t)(rows_s[r] / a.x_div) * a.ldx + k0 + k] : 0.f;
+        ws[k][r] = in && n0 + r < a.N ? a.W[(w0 + n0 + r) * a.K + k0 + k] : 0.f;
       }
       __syncthreads();
 #pragma unroll
@@ -93,17 +67,11 @@ __global__ void __launch_bounds__(kThreads) moe_product_kernel(ProductArgs a) {
     for (int i = 0; i < 4; ++i) {
       const int r = ty * 4 + i;
       if (r >= rows) break;
-      TY *y = static_cast<TY *>(a.y) + (int64_t)rows_s[r] * a.ldy;
+      float *y = a.y + (int64_t)rows_s[r] * a.ldy;
       for (int j = 0; j < 4; ++j)
-        if (n0 + tx * 4 + j < a.N) y[n0 + tx * 4 + j] = Elem<TY>::from_f(acc[i][j]);
+        if (n0 + tx * 4 + j < a.N) y[n0 + tx * 4 + j] = acc[i][j];
     }
   }
-}
-
-template <typename Rows>
-cudaError_t launch(const ProductArgs &a, dim3 grid, int y_dtype, cudaStream_t st) {
-  return launch_pdl(y_dtype == LORA_BF16 ? moe_product_kernel<Rows, __nv_bfloat16> : moe_product_kernel<Rows, float>,
-                    grid, dim3(kThreads), 0, st, 1u, a);
 }
 
 }  // namespace
@@ -111,15 +79,14 @@ cudaError_t launch(const ProductArgs &a, dim3 grid, int y_dtype, cudaStream_t st
 cudaError_t launch_moe_product(const lora_expert_desc &d, const MetaView &mv, const void *x, int64_t ldx,
                                const uint8_t *x_scale, int64_t ld_xs, void *y, int64_t ldy, int y_dtype,
                                cudaStream_t st) {
-  const ProductArgs a{x, d.W, x_scale, d.W_scale, ldx, ld_xs, d.ld_scale, ldy, y, mv.work, mv.sorted_rows,
-                      mv.num_slots, d.d_in, d.d_out, std::max(1, d.x_row_div)};
   const int64_t tiles = (int64_t)mv.num_tokens / LORA_SGMV_TILE_M + std::min(mv.num_slots - 1, mv.num_tokens);
   if (tiles == 0) return cudaSuccess;
+  if (d.dtype != LORA_F32) return launch_moe_product_tc(d, mv, x, ldx, x_scale, ld_xs, y, ldy, y_dtype, st);
+  const ProductArgs a{static_cast<const float *>(x), static_cast<const float *>(d.W), ldx, ldy, static_cast<float *>(y),
+                      mv.work, mv.sorted_rows, mv.num_slots, d.d_in, d.d_out, std::max(1, d.x_row_div)};
   const dim3 grid((unsigned)((d.d_out + kTile - 1) / kTile),
                   (unsigned)std::min<int64_t>(tiles * (LORA_SGMV_TILE_M / kTile), 1024));
-  if (d.dtype == LORA_MXFP4) return launch<RowsMx>(a, grid, y_dtype, st);
-  if (d.dtype == LORA_BF16) return launch<RowsBf16>(a, grid, y_dtype, st);
-  return launch<RowsF32>(a, grid, y_dtype, st);
+  return launch_pdl(moe_product_kernel, grid, dim3(kThreads), 0, st, 1u, a);
 }
 
 }  // namespace ra

@@ -29,14 +29,11 @@
 // Every wait on a barrier is bounded: one that runs out records an error in
 // the work-list header (reported by lora_query_status) and the CTA winds
 // down without touching memory it does not own.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <cstring>
 #include <map>
 #include <mutex>
 
-#include "common.cuh"
+#include "tcgen05.cuh"
 
 namespace ra {
 namespace {
@@ -46,209 +43,13 @@ constexpr int kKB = 64;                   // d_in elements per shrink K block (o
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kAlignSlack = 1024;         // dynamic smem is re-aligned to 1024 bytes
 constexpr int kUKRegion = kTileM * 128;   // bytes of one 64-wide K region of a 128-row operand
-constexpr uint64_t kWaitNs = 200000000ull;  // a pipeline wait longer than 200 ms means a fault
 
 // Error bits in the work-list header (word WorkLists::kErrWord).
 constexpr int kErrShrink = 1;
 constexpr int kErrExpand = 2;
 constexpr int kErrProbe = 4;  // lora_probe_bounded_wait
 
-// Shared-memory descriptor layouts.
-constexpr uint32_t kSw128 = 2, kSw64 = 4, kSw32 = 6;
 
-// ------------------------------------------------------------------ PTX wrappers
-
-__device__ __forceinline__ void mbar_init(uint64_t *b, uint32_t n) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(n) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t *b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_tx(uint64_t *b, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(b)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint64_t *b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_addr(b)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ uint64_t global_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-// Wait for the phase of the given parity. Gives up after limit_ns (by
-// default kWaitNs): records `code` in *err and returns false.
-__device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity, int *err, int code,
-                                          uint64_t limit_ns = kWaitNs) {
-  if (mbar_try(b, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (;;) {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try(b, parity)) return true;
-    if (global_ns() - t0 > limit_ns) {
-      atomicOr(err, code);
-      return false;
-    }
-  }
-}
-// The same, with one verdict for the whole warp (every lane must call it).
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t *b, uint32_t parity, int *err, int code) {
-  return __all_sync(0xffffffffu, mbar_wait(b, parity, err, code)) != 0;
-}
-__device__ __forceinline__ void fence_mbar_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
-// Order this thread's generic-proxy shared-memory writes before later async-proxy reads.
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void tc_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int c0, int c1, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-      ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_addr(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-      ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
-      : "memory");
-}
-// 16-byte cp.async that writes zeros when !valid (nothing is read then).
-__device__ __forceinline__ void cp_async16_zfill(void *dst, const void *src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-               ::"r"(smem_addr(dst)), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-
-// TMEM: allocation by one whole warp; the address lands in shared memory.
-__device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
-               ::"r"(smem_addr(slot)), "r"(ncols) : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_free(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-// MMAs are issued by one elected lane of a converged warp, the way the
-// instruction wants its operands (warp-uniform values). A whole 64-deep K
-// block (four 16-deep steps) goes out from one asm block: its descriptors are
-// formed once and advanced in place, A by a_step and B by b_step (16-byte
-// units), so no other instruction sits between the MMAs and the tensor pipe
-// stays fed. Timed on this part: back-to-back issue like this keeps an
-// M=128 MMA at its pipe rate; with the descriptors rebuilt between MMAs by a
-// single divergent lane, issue alone took several times the MMA itself.
-// The first MMA accumulates when `acc` is non-zero; the others always do.
-// Every lane of the warp must call these.
-template <int kSteps>
-__device__ __forceinline__ void mma_run(uint32_t d, uint64_t ad, uint64_t bd, uint64_t a_step, uint64_t b_step,
-                                        uint32_t idesc, uint32_t acc) {
-  static_assert(kSteps == 1 || kSteps == 2 || kSteps == 4, "1, 2 or 4 steps");
-  if constexpr (kSteps == 1) {
-    asm volatile(
-        "{\n\t.reg .pred q, e;\n\t.reg .b32 r;\n\t"
-        "elect.sync r|e, 0xffffffff;\n\tsetp.ne.b32 q, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t}"
-        ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "l"(a_step), "l"(b_step)
-        : "memory");
-  } else if constexpr (kSteps == 2) {
-    asm volatile(
-        "{\n\t.reg .pred q, e, t;\n\t.reg .b32 r;\n\t.reg .b64 a1, b1;\n\t"
-        "elect.sync r|e, 0xffffffff;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 t, %3, %3;\n\t"
-        "add.s64 a1, %1, %5;\n\tadd.s64 b1, %2, %6;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t}"
-        ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "l"(a_step), "l"(b_step)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred q, e, t;\n\t.reg .b32 r;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-        "elect.sync r|e, 0xffffffff;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 t, %3, %3;\n\t"
-        "add.s64 a1, %1, %5;\n\tadd.s64 a2, a1, %5;\n\tadd.s64 a3, a2, %5;\n\t"
-        "add.s64 b1, %2, %6;\n\tadd.s64 b2, b1, %6;\n\tadd.s64 b3, b2, %6;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}"
-        ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(acc), "l"(a_step), "l"(b_step)
-        : "memory");
-  }
-}
-// 1, 2 or 4 steps chosen at run time (a warp-uniform value).
-__device__ __forceinline__ void mma_steps(int steps, uint32_t d, uint64_t ad, uint64_t bd, uint64_t a_step,
-                                          uint64_t b_step, uint32_t idesc, uint32_t acc) {
-  if (steps >= 4) mma_run<4>(d, ad, bd, a_step, b_step, idesc, acc);
-  else if (steps == 2) mma_run<2>(d, ad, bd, a_step, b_step, idesc, acc);
-  else mma_run<1>(d, ad, bd, a_step, b_step, idesc, acc);
-}
-// D[tmem] (+)= A[smem] * B[smem] with bf16 operands and an fp32 accumulator
-// is what each MMA computes. tcgen05.commit, below, gives the barrier one
-// arrival once every MMA the committing lane issued so far is complete; it is
-// sent from the elected lane, the one that issued the MMAs.
-__device__ __forceinline__ void mma_commit_elect(uint64_t *bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
-      ::"r"(smem_addr(bar)) : "memory");
-}
-
-// 16 consecutive fp32 accumulator columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// 32 consecutive fp32 accumulator columns, without waiting (see tmem_wait_ld).
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float *v) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-// Shared-memory matrix descriptor (start, leading / stride byte offsets, swizzle).
-// For the swizzled MN-major operands here the leading offset is the distance
-// between blocks along N and the stride offset the distance between groups of
-// 8 rows along K; for the K-major ones the stride offset is the distance
-// between groups of 8 rows (the leading offset is unused).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | ((uint64_t)layout << 61);
-}
-// Instruction descriptor of kind::f16: fp32 accumulator, bf16 A and B, A K-major, B MN-major.
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-// Byte offset of 16-byte chunk c of row r in a 128-row, 128-byte-swizzled K-major region.
-__device__ __forceinline__ uint32_t swz128(int r, int c) {
-  return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
-}
-
-__device__ __forceinline__ unsigned char *align1024(unsigned char *p) {
-  return reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~(uintptr_t)1023);
-}
 
 // ------------------------------------------------------------------ work items
 
@@ -1131,33 +932,6 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 }
 
 // ------------------------------------------------------------------ host side
-
-int sm_count() {
-  static std::mutex mu;
-  static std::map<int, int> cache;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  auto it = cache.find(dev);
-  if (it != cache.end()) return it->second;
-  int n = 0;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  cache[dev] = n;
-  return n;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static std::once_flag once;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
 
 // 3-D bf16 tensor map {d0 (contiguous), d1, d2} with a {box0, box1, 1} box.
 cudaError_t make_map(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t box0,
