@@ -385,13 +385,13 @@ int lora_moe_route(const void *logits, int64_t ld_logits, int32_t dtype, int32_t
  *   W: device, [num_experts, d_out, d_in] row-major, d_in contiguous. LORA_F32
  *      (accuracy runs), LORA_BF16, or LORA_MXFP4: two elements a byte as
  *      lora_mx_quantize writes them, d_in / 2 bytes a row.
- *   W_scale, ld_scale: LORA_MXFP4 only: scale bytes [num_experts, d_out] rows
- *      of ld_scale bytes (d_in / LORA_MX_BLOCK of them used).
+ *   W_scale: LORA_MXFP4 only: the scale bytes as lora_mx_tile_scales lays them
+ *      out, lora_mx_tiles_bytes(num_experts, d_out, d_in) bytes.
  *   x_row_div: pair p reads x row p / x_row_div (0 or 1: row p), as in
  *      lora_layer_desc; a w13 projection sets topk.
  * Constraints: 1 <= num_experts < LORA_MAX_NUM_SLOTS; d_in and d_out positive
  * multiples of 8 (d_in of LORA_MX_BLOCK for LORA_MXFP4); W and W_scale 16-byte
- * aligned, ld_scale a multiple of 16 and at least d_in / LORA_MX_BLOCK.
+ * aligned.
  */
 typedef struct {
   int32_t dtype;
@@ -400,7 +400,6 @@ typedef struct {
   int32_t num_experts;
   const void *W;
   const uint8_t *W_scale;
-  int64_t ld_scale;
   int32_t x_row_div;
 } lora_expert_desc;
 
@@ -451,6 +450,22 @@ int lora_mx_quantize(const void *x, int64_t ldx, int32_t x_dtype, int64_t rows, 
  * as lora_mx_quantize. */
 int lora_mx_dequantize(const uint8_t *codes, int64_t ld_codes, const uint8_t *scales, int64_t ld_scales, int64_t rows,
                        int32_t cols, void *y, int64_t ldy, int32_t y_dtype, lora_stream_t stream);
+
+/*
+ * The scale bytes of experts' 4-bit weights, laid out once for
+ * lora_moe_product: scales is [num_experts * d_out] rows of ld_scales bytes
+ * (lora_mx_quantize of the weights' rows), tiles gets, for every expert, every
+ * 128 outputs and every 128 elements of d_in (in that order; outputs and
+ * elements padded to 128 and 256 with the byte of scale 1), the 512 bytes
+ * [output % 32][output / 32 % 4][block of 32 elements].
+ * Errors as lora_mx_quantize; num_experts outside [1, LORA_MAX_NUM_SLOTS) ->
+ * LORA_ERANGE.
+ */
+int lora_mx_tile_scales(const uint8_t *scales, int64_t ld_scales, int32_t num_experts, int32_t d_out, int32_t d_in,
+                        uint8_t *tiles, lora_stream_t stream);
+
+/* Bytes of the tiles of lora_mx_tile_scales; 0 for invalid sizes. */
+size_t lora_mx_tiles_bytes(int32_t num_experts, int32_t d_out, int32_t d_in);
 
 /*
  * The gated activation between w13 and w2, for every pair with pair_slot > 0

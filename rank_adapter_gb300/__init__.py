@@ -30,7 +30,8 @@ __all__ = [
     "lora_shrink_noalloc", "lora_noalloc_scratch_bytes", "lora_embed_shrink", "embed_shrink",
     "lora_moe_pair_slots", "moe_pair_slots",
     "LORA_MXFP4", "LORA_SCORE_SOFTMAX", "LORA_SCORE_SIGMOID", "LORA_MAX_EXPERTS", "LORA_MAX_ROUTE_TOPK", "LORA_MX_BLOCK",
-    "lora_moe_route", "lora_moe_product", "lora_mx_quantize", "lora_mx_dequantize", "lora_moe_act", "lora_moe_act_mx",
+    "lora_moe_route", "lora_moe_product", "lora_mx_quantize", "lora_mx_dequantize",
+    "lora_mx_tile_scales", "lora_mx_tiles_bytes", "lora_moe_act", "lora_moe_act_mx",
     "lora_moe_combine", "ExpertDesc", "ExpertWeights", "moe_route", "moe_product", "mx4_buffers", "mx4_quantize",
     "mx4_dequantize", "moe_act", "moe_act_mx4", "moe_combine",
     "lora_workspace_bytes", "lora_meta_tiles_bytes", "lora_query_status", "lora_probe_bounded_wait", "lora_strerror",
@@ -98,7 +99,7 @@ class ExpertDesc(ctypes.Structure):
     """lora_expert_desc: one projection's expert weights (device pointers)."""
     _fields_ = [
         ("dtype", _i32), ("d_in", _i32), ("d_out", _i32), ("num_experts", _i32),
-        ("W", _vp), ("W_scale", _vp), ("ld_scale", ctypes.c_int64), ("x_row_div", _i32),
+        ("W", _vp), ("W_scale", _vp), ("x_row_div", _i32),
     ]
 
 
@@ -126,6 +127,8 @@ _sig = {
     "lora_moe_product": (_i32, [_P(ExpertDesc), _P(Meta), _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp]),
     "lora_mx_quantize": (_i32, [_vp, _i64, _i32, _i64, _i32, _vp, _i64, _vp, _i64, _vp]),
     "lora_mx_dequantize": (_i32, [_vp, _i64, _vp, _i64, _i64, _i32, _vp, _i64, _i32, _vp]),
+    "lora_mx_tile_scales": (_i32, [_vp, _i64, _i32, _i32, _i32, _vp, _vp]),
+    "lora_mx_tiles_bytes": (ctypes.c_size_t, [_i32, _i32, _i32]),
     "lora_moe_act": (_i32, [_vp, _i64, _i32, _vp, _i32, _i32, _vp, _i64, _i32, _vp]),
     "lora_moe_act_mx": (_i32, [_vp, _i64, _i32, _vp, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
     "lora_moe_combine": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _i64, _i32, _i32, _vp]),
@@ -245,6 +248,15 @@ def lora_mx_dequantize(codes: int, ld_codes: int, scales: int, ld_scales: int, r
                        y_dtype: int, stream=None) -> int:
     return _lib.lora_mx_dequantize(codes or None, ld_codes, scales or None, ld_scales, rows, cols, y or None, ldy,
                                    y_dtype, _stream(stream))
+
+
+def lora_mx_tile_scales(scales: int, ld_scales: int, num_experts: int, d_out: int, d_in: int, tiles: int,
+                        stream=None) -> int:
+    return _lib.lora_mx_tile_scales(scales or None, ld_scales, num_experts, d_out, d_in, tiles or None, _stream(stream))
+
+
+def lora_mx_tiles_bytes(num_experts: int, d_out: int, d_in: int) -> int:
+    return int(_lib.lora_mx_tiles_bytes(num_experts, d_out, d_in))
 
 
 def lora_moe_act(y13: int, ldy: int, y_dtype: int, pair_slot: int, num_pairs: int, inter: int, h: int, ldh: int,
@@ -515,11 +527,12 @@ class ExpertWeights:
     """The local experts' weights of one projection, in caller-owned torch memory.
 
     ``w``: [num_experts, d_out, d_in] bf16 or fp32, or the 4-bit codes [num_experts, d_out, d_in / 2]
-    uint8 with ``scale`` [num_experts, d_out, ld] uint8 (``mx4_quantize`` of the weights' rows). ``x_row_div``:
-    pair p reads x row p // x_row_div (a w13 projection: topk).
+    uint8 with ``scale`` [num_experts, d_out, ld] uint8 (``mx4_quantize`` of the weights' rows), which the
+    constructor lays out in tiles (lora_mx_tile_scales, on ``stream``) and does not keep. ``x_row_div``: pair p
+    reads x row p // x_row_div (a w13 projection: topk).
     """
 
-    def __init__(self, w, scale=None, x_row_div: int = 1):
+    def __init__(self, w, scale=None, x_row_div: int = 1, stream=None):
         import torch
         if w.dim() != 3 or not w.is_contiguous():
             raise ValueError(f"ExpertWeights: expected contiguous [experts, d_out, d_in] weights, got {tuple(w.shape)}")
@@ -531,7 +544,10 @@ class ExpertWeights:
                 raise ValueError("ExpertWeights: 4-bit weights are uint8 codes [experts, d_out, d_in / 2] and contiguous "
                                  "uint8 scales [experts, d_out, ld]")
             d.dtype, d.d_in = LORA_MXFP4, 2 * w.shape[2]
-            d.W_scale, d.ld_scale = scale.data_ptr(), scale.shape[2]
+            tiles = torch.empty(lora_mx_tiles_bytes(d.num_experts, d.d_out, d.d_in), dtype=torch.uint8, device=w.device)
+            check(lora_mx_tile_scales(scale.data_ptr(), scale.shape[2], d.num_experts, d.d_out, d.d_in,
+                                      tiles.data_ptr(), stream), "lora_mx_tile_scales")
+            d.W_scale, scale = tiles.data_ptr(), tiles
         else:
             d.dtype = _dt(w)
         d.W, d.x_row_div = w.data_ptr(), x_row_div

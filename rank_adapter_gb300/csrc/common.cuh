@@ -72,6 +72,47 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
   reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
+// Eight consecutive elements as loaded, for kernels that request several
+// vectors before they widen the first.
+template <typename T> struct Raw8 { uint4 u[sizeof(T) / 2]; };
+template <typename T> __device__ __forceinline__ Raw8<T> raw8(const T *p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.u[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+  return r;
+}
+__device__ __forceinline__ void widen8(const Raw8<__nv_bfloat16> &r, float (&v)[8]) {
+  const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&r.u[0]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __bfloat1622float2(h[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void widen8(const Raw8<float> &r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[4 * i] = __uint_as_float(r.u[i].x);
+    v[4 * i + 1] = __uint_as_float(r.u[i].y);
+    v[4 * i + 2] = __uint_as_float(r.u[i].z);
+    v[4 * i + 3] = __uint_as_float(r.u[i].w);
+  }
+}
+
+// Launch shape of kernels that work on rows of `chunks` eight-element chunks,
+// `per_thread` rows a thread: CTAs of `threads` as threads along a row (a
+// power of two of at least 4) by rows.
+struct RowGrid {
+  dim3 grid, block;
+  static RowGrid of(int64_t rows, int chunks, int threads, int per_thread) {
+    int tx = 4;
+    while (tx < threads && tx < chunks) tx *= 2;
+    const int64_t ty = threads / tx, step = ty * per_thread;
+    return {dim3((unsigned)((chunks + tx - 1) / tx), (unsigned)std::min<int64_t>((rows + step - 1) / step, 65535)),
+            dim3((unsigned)tx, (unsigned)ty)};
+  }
+};
 // ------------------------------------------------------------------ cluster / shared memory
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -271,6 +312,8 @@ cudaError_t launch_moe_product(const lora_expert_desc &d, const MetaView &mv, co
 cudaError_t launch_moe_product_tc(const lora_expert_desc &d, const MetaView &mv, const void *x, int64_t ldx,
                                   const uint8_t *x_scale, int64_t ld_xs, void *y, int64_t ldy, int y_dtype,
                                   cudaStream_t st);  // bf16 and 4-bit weights (moe_product_tc.cu)
+cudaError_t launch_mx_tile_scales(const uint8_t *scales, int64_t lds, int experts, int d_out, int d_in, uint8_t *tiles,
+                                  cudaStream_t st);
 cudaError_t launch_mx_quantize(const void *x, int64_t ldx, int x_dtype, int64_t rows, int cols, uint8_t *codes,
                                int64_t ldc, uint8_t *scales, int64_t lds, cudaStream_t st);
 cudaError_t launch_mx_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t lds, int64_t rows,

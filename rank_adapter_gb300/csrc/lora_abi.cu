@@ -8,7 +8,7 @@
 #include <map>
 #include <utility>
 
-#include "common.cuh"
+#include "mx.cuh"
 
 namespace ra {
 
@@ -444,8 +444,8 @@ int lora_moe_product(const lora_expert_desc *desc, const lora_meta *meta, const 
   if (!aligned16(desc->W)) return LORA_EALIGN;
   const int64_t blocks = desc->d_in / LORA_MX_BLOCK;
   if (mx) {
-    if (desc->W_scale == nullptr || desc->ld_scale < blocks) return LORA_EINVAL;
-    if (!aligned16(desc->W_scale) || desc->ld_scale % 16 != 0) return LORA_EALIGN;
+    if (desc->W_scale == nullptr) return LORA_EINVAL;
+    if (!aligned16(desc->W_scale)) return LORA_EALIGN;
   }
   int st = check_meta(meta);
   if (st != LORA_OK) return st;
@@ -481,6 +481,21 @@ int lora_mx_dequantize(const uint8_t *codes, int64_t ld_codes, const uint8_t *sc
   if (st != LORA_OK || rows == 0) return st;
   return cuda_status(ra::launch_mx_dequantize(codes, ld_codes, scales, ld_scales, rows, cols, y, ldy, y_dtype,
                                               (cudaStream_t)stream));
+}
+
+size_t lora_mx_tiles_bytes(int32_t num_experts, int32_t d_out, int32_t d_in) {
+  if (num_experts < 1 || num_experts >= LORA_MAX_NUM_SLOTS || d_out < 1 || d_in < 1) return 0;
+  return (size_t)num_experts * ra::mx_tiles_out(d_out) * ra::mx_tiles_in(d_in) * ra::kMxTileBytes;
+}
+
+int lora_mx_tile_scales(const uint8_t *scales, int64_t ld_scales, int32_t num_experts, int32_t d_out, int32_t d_in,
+                        uint8_t *tiles, lora_stream_t stream) {
+  clear_stale_error();
+  if (num_experts < 1 || num_experts >= LORA_MAX_NUM_SLOTS) return LORA_ERANGE;
+  if (d_out < 8 || d_out % 8 != 0 || d_in < LORA_MX_BLOCK || d_in % LORA_MX_BLOCK != 0) return LORA_EINVAL;
+  if (scales == nullptr || tiles == nullptr || ld_scales < d_in / LORA_MX_BLOCK) return LORA_EINVAL;
+  if (!aligned16(scales) || !aligned16(tiles) || ld_scales % 16 != 0) return LORA_EALIGN;
+  return cuda_status(ra::launch_mx_tile_scales(scales, ld_scales, num_experts, d_out, d_in, tiles, (cudaStream_t)stream));
 }
 
 int lora_moe_act(const void *y13, int64_t ldy, int32_t y_dtype, const int32_t *pair_slot, int32_t num_pairs,

@@ -145,27 +145,37 @@ struct ActArgs {
   int P, inter;
 };
 
-__device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
+// For a result that is rounded to bf16 the fast exponential and quotient do
+// (together within |g| * 2^-23 of the value, 2^-9 is rounded away; below -87,
+// where the value is under 1e-35, it may come out as 0); an fp32 result takes
+// the exact ones. At 32744 rows of 2048 the exact ones bind the kernel by
+// instructions (85.1 us, with the fast ones 67.3 us, 0.89 of the measured copy rate; more rows
+// a thread at once changed nothing).
+template <bool kFast> __device__ __forceinline__ float silu(float g) {
+  if constexpr (kFast) return __fdividef(g, 1.f + __expf(-g));
+  else return g / (1.f + expf(-g));
+}
 
-template <typename TY>
-__device__ __forceinline__ void act8(const TY *row, int inter, int c, float (&v)[8]) {
+template <bool kFast, typename TY>
+__device__ __forceinline__ void act8(const ActArgs &a, int64_t p, int c, float (&v)[8]) {
+  const TY *row = static_cast<const TY *>(a.y13) + p * a.ldy + (int64_t)c * 8;
   float u[8];
-  load8_f32(row + c * 8, v);
-  load8_f32(row + inter + c * 8, u);
+  load8_f32(row, v);
+  load8_f32(row + a.inter, u);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = silu(v[i]) * u[i];
+  for (int j = 0; j < 8; ++j) v[j] = silu<kFast>(v[j]) * u[j];
 }
 
 template <typename TY, typename TH>
 __global__ void __launch_bounds__(kThreads) moe_act_kernel(ActArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int chunks = a.inter / 8, c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= chunks) return;
+  const int c = blockIdx.x * blockDim.x + threadIdx.x;
+  if (c >= a.inter / 8) return;
   for (int64_t p = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; p < a.P; p += (int64_t)gridDim.y * blockDim.y) {
     if (a.pair_slot != nullptr && a.pair_slot[p] <= 0) continue;
     float v[8];
-    act8(static_cast<const TY *>(a.y13) + p * a.ldy, a.inter, c, v);
+    act8<sizeof(TH) == 2, TY>(a, p, c, v);
     store8(static_cast<TH *>(a.h) + p * a.ldh + (int64_t)c * 8, v);
   }
 }
@@ -177,17 +187,15 @@ template <typename TY>
 __global__ void __launch_bounds__(kThreads) moe_act_mx_kernel(ActArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int chunks = a.inter / 8, c = blockIdx.x * blockDim.x + threadIdx.x;
+  const int c = blockIdx.x * blockDim.x + threadIdx.x;
   for (int64_t p0 = (int64_t)blockIdx.y * blockDim.y; p0 < a.P; p0 += (int64_t)gridDim.y * blockDim.y) {
     const int64_t p = p0 + threadIdx.y;
     // The four lanes of a block of 32 are in one row and in range together.
-    const bool in = p < a.P && c < chunks && (a.pair_slot == nullptr || a.pair_slot[p] > 0);
+    const bool in = p < a.P && c < a.inter / 8 && (a.pair_slot == nullptr || a.pair_slot[p] > 0);
     float v[8] = {};
-    if (in) {
-      act8(static_cast<const TY *>(a.y13) + p * a.ldy, a.inter, c, v);
+    if (in) act8<true, TY>(a, p, c, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(__float2bfloat16_rn(v[i]));
-    }
+    for (int j = 0; j < 8; ++j) v[j] = __bfloat162float(__float2bfloat16_rn(v[j]));
     uint32_t byte;
     const uint32_t q = mx_quantize8(v, byte);
     if (in) {
@@ -215,53 +223,49 @@ struct CombineArgs {
 };
 
 template <typename TY, typename TO>
-__global__ void __launch_bounds__(kThreads) moe_combine_kernel(CombineArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) moe_combine_kernel(CombineArgs a) {
   pdl_wait();
   pdl_trigger();
   constexpr int kAhead = sizeof(TY) == 2 ? 8 : 4;
-  const int chunks = a.n / 8, c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= chunks) return;
+  const int chunks = a.n / 8;
   for (int64_t t = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; t < a.T; t += (int64_t)gridDim.y * blockDim.y) {
-    TO *o = static_cast<TO *>(a.out) + t * a.ldo + (int64_t)c * 8;
-    float acc[8] = {};
-    if (a.accumulate) load8_rw(o, acc);
     const float *w = a.w + t * a.topk;
     const int32_t *slot = a.pair_slot != nullptr ? a.pair_slot + t * a.topk : nullptr;
-    const TY *y = static_cast<const TY *>(a.y) + t * a.topk * a.ldy + (int64_t)c * 8;
-    for (int k0 = 0; k0 < a.topk; k0 += kAhead) {
-      float v[kAhead][8], wk[kAhead];
-      bool live[kAhead];
+    for (int c = blockIdx.x * blockDim.x + threadIdx.x; c < chunks; c += gridDim.x * blockDim.x) {
+      TO *o = static_cast<TO *>(a.out) + t * a.ldo + (int64_t)c * 8;
+      float acc[8] = {};
+      if (a.accumulate) load8_rw(o, acc);
+      const TY *y = static_cast<const TY *>(a.y) + t * a.topk * a.ldy + (int64_t)c * 8;
+      for (int k0 = 0; k0 < a.topk; k0 += kAhead) {
+        Raw8<TY> raw[kAhead];
+        float wk[kAhead];
+        int sk[kAhead];
+        // Slots and weights first, unconditionally: a load behind a branch on
+        // the previous one's value would wait for it.
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int k = k0 + i;
-        live[i] = k < a.topk && (slot == nullptr || slot[k] > 0);
-        if (live[i]) {
-          wk[i] = w[k];
-          load8_f32(y + k * a.ldy, v[i]);
+        for (int i = 0; i < kAhead; ++i) {
+          const int k = min(k0 + i, a.topk - 1);
+          wk[i] = __ldg(w + k);
+          sk[i] = slot != nullptr ? __ldg(slot + k) : 1;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {  // a choice that does not count adds 0 * 0
+          const bool live = k0 + i < a.topk && sk[i] > 0;
+          raw[i] = Raw8<TY>{};
+          if (live) raw[i] = raw8(y + (k0 + i) * a.ldy);
+          wk[i] = live ? wk[i] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          float v[8];
+          widen8(raw[i], v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = fmaf(wk[i], v[j], acc[j]);
         }
       }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (!live[i]) continue;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = fmaf(wk[i], v[i][j], acc[j]);
-      }
+      store8(o, acc);
     }
-    store8(o, acc);
   }
-}
-
-// CTA shape for rows of `chunks` eight-element chunks: threads along a row (a
-// power of two of at least 4) by rows.
-struct Launch {
-  dim3 grid, block;
-};
-Launch shape_of(int64_t rows, int chunks, int threads) {
-  int tx = 4;
-  while (tx < threads && tx < chunks) tx *= 2;
-  const int ty = threads / tx;
-  return {dim3((unsigned)((chunks + tx - 1) / tx), (unsigned)std::min<int64_t>((rows + ty - 1) / ty, 65535)),
-          dim3((unsigned)tx, (unsigned)ty)};
 }
 
 }  // namespace
@@ -276,7 +280,7 @@ cudaError_t launch_moe_route(const void *logits, int64_t ldl, int dtype, int T, 
 cudaError_t launch_moe_act(const void *y13, int64_t ldy, int y_dtype, const int32_t *pair_slot, int P, int inter,
                            void *h, int64_t ldh, int h_dtype, cudaStream_t st) {
   const ActArgs a{y13, ldy, pair_slot, h, ldh, nullptr, 0, P, inter};
-  const Launch l = shape_of(P, inter / 8, kThreads);
+  const RowGrid l = RowGrid::of(P, inter / 8, kThreads, 1);
   void (*k)(ActArgs) =
       y_dtype == LORA_BF16
           ? (h_dtype == LORA_BF16 ? moe_act_kernel<__nv_bfloat16, __nv_bfloat16> : moe_act_kernel<__nv_bfloat16, float>)
@@ -287,7 +291,7 @@ cudaError_t launch_moe_act(const void *y13, int64_t ldy, int y_dtype, const int3
 cudaError_t launch_moe_act_mx(const void *y13, int64_t ldy, int y_dtype, const int32_t *pair_slot, int P, int inter,
                               uint8_t *codes, int64_t ldc, uint8_t *scales, int64_t lds, cudaStream_t st) {
   const ActArgs a{y13, ldy, pair_slot, codes, ldc, scales, lds, P, inter};
-  const Launch l = shape_of(P, inter / 8, kThreads);
+  const RowGrid l = RowGrid::of(P, inter / 8, kThreads, 1);
   return launch_pdl(y_dtype == LORA_BF16 ? moe_act_mx_kernel<__nv_bfloat16> : moe_act_mx_kernel<float>, l.grid, l.block,
                     0, st, 1u, a);
 }
@@ -296,7 +300,7 @@ cudaError_t launch_moe_combine(const void *y, int64_t ldy, int y_dtype, const fl
                                int topk, int n, void *out, int64_t ldo, int out_dtype, int accumulate,
                                cudaStream_t st) {
   const CombineArgs a{y, ldy, w, pair_slot, out, ldo, T, topk, n, accumulate};
-  const Launch l = shape_of(T, n / 8, kThreads);
+  const RowGrid l = RowGrid::of(T, n / 8, kThreads, 1);
   void (*k)(CombineArgs) = y_dtype == LORA_BF16
                                ? (out_dtype == LORA_BF16 ? moe_combine_kernel<__nv_bfloat16, __nv_bfloat16>
                                                          : moe_combine_kernel<__nv_bfloat16, float>)

@@ -22,6 +22,7 @@
 // rows) and copied to TMEM ahead of each stage's MMAs.
 #include <cstring>
 
+#include "mx.cuh"
 #include "tcgen05.cuh"
 
 namespace ra {
@@ -32,7 +33,19 @@ constexpr int kStepBytes = 128;     // bytes of a row a stage holds: 64 bf16, 25
 constexpr int kRowsA = 128;         // outputs of a CTA
 constexpr int kPairA = 2 * kRowsA;  // outputs of a pair
 constexpr int kBytesA = kRowsA * kStepBytes;
-constexpr int kEpiWarp = 4, kRowWarp = 8, kScaleWarp = 12;  // first of the four epilogue, four x and the scale warps
+
+// Warps of a CTA: 0 weights, 1 passes this CTA's rows on to the leader, 2 MMA,
+// 3 tiles, then four of the epilogue, eight of the x rows and the scale warps.
+constexpr int kRowWarp = 8, kRowWarps = 8, kScaleWarp = kRowWarp + kRowWarps;
+constexpr int kRing = 3;            // tiles described ahead
+
+// A tile as its warps read it.
+template <int TN>
+struct alignas(16) TileInfo {
+  int expert, rows, f0, pad;        // rows of the tile, first output of the pair
+  int x[TN], y[TN];                 // the rows' x rows (past the tile the last one again) and y rows
+  __device__ __forceinline__ int n_pad() const { return (rows + 31) & ~31; }
+};
 
 // Shared-memory layout and TMEM columns of a variant: tiles of up to TN rows,
 // ACC accumulators, STAGES pipeline stages, SW warps that bring scales.
@@ -46,29 +59,34 @@ struct Shape {
   // back, lies within one turn of the pipeline.
   static_assert(MX == (kScaleWarps > 0) && STAGES_ >= 2 * SW_ - 1, "scale warps");
   static constexpr int kBytesB = TN_ / 2 * kStepBytes;
-  static constexpr int kAtomsB = (TN_ + 127) / 128;             // 512-byte scale atoms of a word of the x rows
+  static constexpr int kAtomsB = (TN_ + 127) / 128;              // 512-byte scale atoms of a word of the x rows
   static constexpr int kBytesSf = MX ? 2 * (1 + kAtomsB) * 512 : 0;
   static constexpr int kStageBytes = kBytesA + kBytesB + kBytesSf;
-  static constexpr int kSfCols = MX ? 8 + 8 * kAtomsB : 0;       // TMEM columns of a stage's scales
-  static constexpr int kSfCol = ACC_ * TN_;
-  static constexpr int kUsedCols = kSfCol + STAGES_ * kSfCols;
+  // TMEM: the accumulators, then the scales of kSfSlots stages.
+  static constexpr int kSfCols = MX ? 8 + 8 * kAtomsB : 0, kSfCol = ACC_ * TN_;
+  static constexpr int kSfSlots = MX ? ((512 - kSfCol) / kSfCols < STAGES_ ? (512 - kSfCol) / kSfCols : STAGES_) : 0;
+  static constexpr int kUsedCols = kSfCol + kSfSlots * kSfCols;
   static constexpr int kTmemCols = kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
-  static_assert(kUsedCols <= 512, "TMEM");
-  static constexpr int kBarriers = 3 * STAGES_ + 2 * ACC_ + 1;
-  static size_t smem(int num_slots) {
-    return 1024 + (size_t)STAGES_ * kStageBytes + kBarriers * 8 + 16 + (size_t)(num_slots + 1) * 4;
-  }
+  static_assert(kUsedCols <= 512 && (!MX || kSfSlots >= 2), "TMEM");
+  static constexpr int kBarriers = 3 * STAGES_ + 2 * ACC_ + 2 * kRing + 1;
+  static constexpr int kTurnOff = STAGES_ * kStageBytes;         // the epilogue warps' 32 x 32 blocks
+  static constexpr int kRingOff = kTurnOff + 4 * 32 * 32 * 4;
+  static constexpr int kBarOff = kRingOff + kRing * (int)sizeof(TileInfo<TN_>);
+  static constexpr int kCumOff = kBarOff + kBarriers * 8 + 16;
+  static size_t smem(int num_slots) { return 1024 + kCumOff + (size_t)num_slots * 4; }
+  static_assert(1024 + kCumOff + LORA_MAX_NUM_SLOTS * 4 <= 227 * 1024, "shared memory");
 };
 
 struct TcArgs {
-  const uint8_t *x, *x_scale, *W_scale;
-  int64_t ldx, ld_xs, ld_ws, ldy;  // bytes a row of x and of the scales; elements of y
+  const uint8_t *x, *x_scale;
+  int64_t ldx, ld_xs, ldy;         // bytes a row of x and of the scales; elements of y
   void *y;
   const int32_t *work, *sorted_rows;
   int *err;
   int num_slots, K, N, x_div;
 };
 struct TcMaps {
+  CUtensorMap W_scale;  // {256 words, pairs of tiles}, boxes of one pair (4-bit weights)
   CUtensorMap W;  // {row bytes, d_out, experts}, boxes of 128 bytes x 128 rows
 };
 
@@ -93,6 +111,11 @@ __device__ __forceinline__ void tma_w(uint32_t dst, const CUtensorMap *map, int 
 // One arrival on a barrier of this CTA when the thread's cp.async so far are complete.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_scales(uint32_t dst, const CUtensorMap *map, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c1), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void tmem_alloc2(uint32_t *slot, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -153,52 +176,44 @@ __device__ __forceinline__ uint32_t idesc_mx(int N, uint32_t id) {
          ((uint32_t)(kPairA >> 4) << 24) | (id << 29);
 }
 
-// ------------------------------------------------------------------ tiles
-
-// Row tiles of a segment of `count` pairs: as few as kTN allows, of equal
-// size rounded up to 32 (the last one may be shorter, never empty).
-template <int TN> __device__ __forceinline__ int row_tiles(int count) { return (count + TN - 1) / TN; }
-
-struct Tile {
-  int slot, first, rows, f0;  // first sorted row, rows, first output of the pair
-  __device__ __forceinline__ int n_pad() const { return (rows + 31) & ~31; }
-};
-template <int TN>
-__device__ __forceinline__ Tile tile_at(const int32_t *work, int num_slots, const int32_t *cum, int n_list, int F,
-                                        int64_t t) {
-  int lo = 0, hi = n_list - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((int64_t)cum[mid] * F <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  const int ntt = cum[lo + 1] - cum[lo];
-  const int64_t local = t - (int64_t)cum[lo] * F;
-  const int f = (int)(local / ntt), tt = (int)(local - (int64_t)f * ntt);
-  const int4 rec = *reinterpret_cast<const int4 *>(work + WorkLists::list(num_slots, kListAll) + lo * WorkLists::kRec);
-  const int tr = (((rec.z + ntt - 1) / ntt) + 31) & ~31;
-  Tile r;
-  r.slot = rec.y;
-  r.first = rec.w + tt * tr;
-  r.rows = min(tr, rec.z - tt * tr);
-  r.f0 = f * kPairA;
-  return r;
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
+// 16-byte cp.async to a shared-memory address, zeros when !valid (nothing is read then).
+__device__ __forceinline__ void cp_async16_to(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+
+// Position in a ring of N: the slot, and the parity of the turn.
+template <int N>
+struct Stage {
+  uint32_t s = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == N) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
 
 // ------------------------------------------------------------------ kernel
 
 template <class S, typename TY>
 __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __grid_constant__ TcMaps maps, const TcArgs a) {
   extern __shared__ unsigned char smem_raw[];
+  using Info = TileInfo<S::kTN>;
   unsigned char *sm = align1024(smem_raw);
-  uint64_t *full = reinterpret_cast<uint64_t *>(sm + S::kStages * S::kStageBytes);  // leader's: a stage of both CTAs is in
+  Info *ring = reinterpret_cast<Info *>(sm + S::kRingOff);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sm + S::kBarOff);  // leader's: a stage of both CTAs is in
   uint64_t *empty = full + S::kStages;  // the stage's MMAs are done
   uint64_t *rows = empty + S::kStages;  // this CTA's x rows (and scales) of a stage are in
   uint64_t *accf = rows + S::kStages;   // an accumulator is complete
   uint64_t *acce = accf + S::kAcc;      // leader's: both CTAs have read it
-  uint64_t *fin = acce + S::kAcc;
+  uint64_t *tfull = acce + S::kAcc;     // a tile is described
+  uint64_t *tempty = tfull + kRing;     // every warp has what it needs of it
+  uint64_t *fin = tempty + kRing;
   uint32_t *tslot = reinterpret_cast<uint32_t *>(fin + 1);
-  int32_t *cum = reinterpret_cast<int32_t *>(tslot + 4);
+  int32_t *cum = reinterpret_cast<int32_t *>(sm + S::kCumOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   if (threadIdx.x == 0) {
@@ -211,25 +226,32 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
       mbar_init(&accf[i], 1);
       mbar_init(&acce[i], 8);
     }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 1 + (rank == 0 ? 1 : 0) + 4 + kRowWarps + S::kScaleWarps);
+    }
     mbar_init(fin, 1);
     fence_mbar_init();
   }
   if (warp == 2) tmem_alloc2(tslot, S::kTmemCols);
+  if (warp == 0 && lane == 0) prefetch_map(&maps.W);
   pdl_wait();
   pdl_trigger();
-  const int n_list = a.work[0];
-  if (warp == 3) {  // row tiles before each segment
+  const int32_t *list = a.work + WorkLists::list(a.num_slots, kListAll);
+  if (warp == 3) {  // row tiles before each segment: as few as kTN allows
+    const int n_list = a.work[0];
     int base = 0;
     for (int i0 = 0; i0 < n_list; i0 += 32) {
       const int i = i0 + lane;
-      const int c = i < n_list ? row_tiles<S::kTN>(a.work[WorkLists::list(a.num_slots, kListAll) + i * WorkLists::kRec + 2]) : 0;
-      int incl = c;
+      const int c = i < a.num_slots ? list[i * WorkLists::kRec + 2] : 0;  // unused records hold -1
+      int incl = c > 0 ? (c + S::kTN - 1) / S::kTN : 0;
+      const int mine = incl;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
-      if (i < n_list) cum[i] = base + incl - c;
+      if (i < n_list) cum[i] = base + incl - mine;
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) cum[n_list] = base;
@@ -238,27 +260,39 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
   cluster_sync();  // also a CTA barrier: cum, the barriers and the TMEM address are visible
   tc_after_sync();
   const uint32_t tmem = *tslot;
-  const int F = (a.N + kPairA - 1) / kPairA;
-  const int64_t n_tiles = (int64_t)cum[n_list] * F;
+  const int F = (a.N + kPairA - 1) / kPairA, n_list = a.work[0];
   const int row_bytes = S::kMx ? a.K / 2 : a.K * 2;
   const int nkb = (row_bytes + kStepBytes - 1) / kStepBytes;
-  const int64_t t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
-  auto tile = [&](int64_t t) { return tile_at<S::kTN>(a.work, a.num_slots, cum, n_list, F, t); };
+  const int64_t n_tiles = (int64_t)cum[n_list] * F, t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
+  const uint32_t n_items = n_tiles > t0 ? (uint32_t)((n_tiles - t0 + dt - 1) / dt) : 0u;  // tiles of this pair
   constexpr int kElemsPerStep = S::kMx ? kStepBytes : kStepBytes / 2;  // in units of the tensor maps' elements
+  // Item `item` of this pair, once it is described (nullptr: the wait ran out), and its release.
+  auto tile = [&](uint32_t item) -> const Info * {
+    return mbar_wait_warp(&tfull[item % kRing], (item / kRing) & 1, a.err, kErrProduct) ? &ring[item % kRing] : nullptr;
+  };
+  auto release = [&](uint32_t item) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&tempty[item % kRing]);
+  };
 
   if (warp == 0) {
     // ---- weights
-    uint32_t it = 0;
+    Stage<S::kStages> st;
     bool ok = true;
-    for (int64_t t = t0; t < n_tiles && ok; t += dt) {
-      const Tile ti = tile(t);
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const uint32_t s = it % S::kStages;
-        if (!mbar_wait_warp(&empty[s], ((it / S::kStages) & 1) ^ 1, a.err, kErrProduct)) { ok = false; break; }
+    for (uint32_t item = 0; item < n_items && ok; ++item) {
+      const Info *ti = tile(item);
+      if (ti == nullptr) break;
+      const int f = ti->f0 + (int)rank * kRowsA, e = ti->expert;
+      // The first pair of the CTA's scale tiles; outputs past the last tile take that one's (they are not stored).
+      const int sf = S::kMx ? (e * mx_tiles_out(a.N) + min(f / kMxTile, mx_tiles_out(a.N) - 1)) * (mx_tiles_in(a.K) / 2) : 0;
+      release(item);
+      for (int kb = 0; kb < nkb; ++kb, st.next()) {
+        if (!mbar_wait_warp(&empty[st.s], st.phase ^ 1, a.err, kErrProduct)) { ok = false; break; }
         if (lane == 0) {
-          if (rank == 0) mbar_arrive_tx(&full[s], 2 * kBytesA);
-          tma_w(smem_addr(sm + s * S::kStageBytes), &maps.W, kb * kElemsPerStep, ti.f0 + (int)rank * kRowsA,
-                ti.slot - 1, leader_addr(&full[s]));
+          if (rank == 0) mbar_arrive_tx(&full[st.s], 2 * (kBytesA + (S::kMx ? 2 * kMxTileBytes : 0)));
+          if constexpr (S::kMx)
+            tma_scales(smem_addr(sm + st.s * S::kStageBytes + kBytesA + S::kBytesB), &maps.W_scale, sf + kb, leader_addr(&full[st.s]));
+          tma_w(smem_addr(sm + st.s * S::kStageBytes), &maps.W, kb * kElemsPerStep, f, e, leader_addr(&full[st.s]));
         }
         __syncwarp();
       }
@@ -267,34 +301,43 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
     // ---- passes this CTA's rows on to the leader. The rows were written by
     // ordinary stores and cp.async; the fence orders them before the tensor
     // core's reads.
-    uint32_t it = 0;
-    bool ok = true;
-    for (int64_t t = t0; t < n_tiles && ok; t += dt)
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const uint32_t s = it % S::kStages;
-        if (!mbar_wait_warp(&rows[s], (it / S::kStages) & 1, a.err, kErrProduct)) { ok = false; break; }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(leader_addr(&full[s]));
-      }
+    Stage<S::kStages> st;
+    const uint64_t n = (uint64_t)n_items * nkb;
+    for (uint64_t i = 0; i < n; ++i, st.next()) {
+      if (!mbar_wait_warp(&rows[st.s], st.phase, a.err, kErrProduct)) break;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(leader_addr(&full[st.s]));
+    }
   } else if (warp == 2) {
     // ---- MMA issue (leader)
     if (rank == 0) {
-      uint32_t it = 0, item = 0;
+      Stage<S::kStages> st;
+      uint32_t it = 0;
       bool ok = true;
-      for (int64_t t = t0; t < n_tiles && ok; t += dt, ++item) {
-        const int n = tile(t).n_pad();
+      for (uint32_t item = 0; item < n_items && ok; ++item) {
+        const Info *ti = tile(item);
+        if (ti == nullptr) break;
+        const int n = ti->n_pad();
+        release(item);
         const uint32_t acc = item % S::kAcc, d = tmem + acc * S::kTN;
         if (!mbar_wait_warp(&acce[acc], ((item / S::kAcc) & 1) ^ 1, a.err, kErrProduct)) break;
         tc_after_sync();
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const uint32_t s = it % S::kStages;
-          if (!mbar_wait_warp(&full[s], (it / S::kStages) & 1, a.err, kErrProduct)) { ok = false; break; }
+        for (int kb = 0; kb < nkb; ++kb, ++it, st.next()) {
+          if (!mbar_wait_warp(&full[st.s], st.phase, a.err, kErrProduct)) { ok = false; break; }
+          if constexpr (S::kSfSlots < S::kStages && S::kMx)
+            // The scales of kSfSlots stages are in TMEM; a slot is free once the
+            // MMAs that many stages back are done.
+            if (it >= (uint32_t)S::kSfSlots) {
+              const uint32_t was = it - S::kSfSlots;
+              if (!mbar_wait_warp(&empty[was % S::kStages], (was / S::kStages) & 1, a.err, kErrProduct)) { ok = false; break; }
+            }
           tc_after_sync();
-          const uint32_t st = smem_addr(sm + s * S::kStageBytes);
-          const uint64_t ad = smem_desc(st, 16, 1024, kSw128), bd = smem_desc(st + kBytesA, 16, 1024, kSw128);
+          const uint32_t at = smem_addr(sm + st.s * S::kStageBytes);
+          const uint64_t ad = smem_desc(at, 16, 1024, kSw128), bd = smem_desc(at + kBytesA, 16, 1024, kSw128);
           if constexpr (S::kMx) {
-            const uint32_t sf = st + kBytesA + S::kBytesB, sa = tmem + S::kSfCol + s * S::kSfCols, sb = sa + 8;
+            const uint32_t sf = at + kBytesA + S::kBytesB;
+            const uint32_t sa = tmem + S::kSfCol + it % S::kSfSlots * S::kSfCols, sb = sa + 8;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               scales_to_tmem(sa + 4 * w, smem_desc(sf + w * 512, 16, 128, 0));
@@ -306,123 +349,173 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
           } else {
             mma_stage_bf16(d, ad, bd, idesc_bf16_kk(n), kb > 0);
           }
-          mma_commit2(&empty[s]);
+          mma_commit2(&empty[st.s]);
         }
         if (ok) mma_commit2(&accf[acc]);
       }
       mma_commit2(fin);
       mbar_wait_warp(fin, 0, a.err, kErrProduct);  // every MMA is done before either CTA leaves
     }
-  } else if (warp >= kEpiWarp && warp < kEpiWarp + 4) {
-    // ---- accumulator -> y: a lane holds an output, a column a row
+  } else if (warp == 3) {
+    // ---- describes the pair's tiles, kRing ahead of the slowest warp. A
+    // segment's row tiles are of equal size rounded up to 32 (the last one may
+    // be shorter, never empty); tiles run in (segment, outputs, rows) order.
+    for (uint32_t item = 0; item < n_items; ++item) {
+      const int64_t t = t0 + (int64_t)item * dt;
+      int lo = 0, hi = n_list - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((int64_t)cum[mid] * F <= t) lo = mid;
+        else hi = mid - 1;
+      }
+      const int4 rec = *reinterpret_cast<const int4 *>(list + lo * WorkLists::kRec);  // segment, slot, pairs, first sorted row
+      const int ntt = cum[lo + 1] - cum[lo];
+      const int64_t local = t - (int64_t)cum[lo] * F;
+      const int f = (int)(local / ntt), tt = (int)(local - (int64_t)f * ntt);
+      const int tr = (((rec.z + ntt - 1) / ntt) + 31) & ~31, n = min(tr, rec.z - tt * tr);
+      if (!mbar_wait_warp(&tempty[item % kRing], ((item / kRing) & 1) ^ 1, a.err, kErrProduct)) break;
+      Info &ti = ring[item % kRing];
+      if (lane == 0) {
+        ti.expert = rec.y - 1;
+        ti.rows = n;
+        ti.f0 = f * kPairA;
+      }
+      int p[S::kTN / 32];
+#pragma unroll
+      for (int g = 0; g < S::kTN / 32; ++g) p[g] = a.sorted_rows[rec.w + tt * tr + min(32 * g + lane, n - 1)];
+#pragma unroll
+      for (int g = 0; g < S::kTN / 32; ++g) {
+        ti.x[32 * g + lane] = p[g] / a.x_div;
+        ti.y[32 * g + lane] = p[g];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tfull[item % kRing]);
+    }
+  } else if (warp < kRowWarp) {
+    // ---- accumulator -> y. A lane reads one output of 32 rows; the warp turns
+    // them round in shared memory (32 rows of 32 outputs) so that a row leaves
+    // in 16-byte pieces (stored from the lanes, two bytes each, the w2 prefill
+    // took 669 us instead of 558).
+    constexpr int kVec = 16 / sizeof(TY), kPieces = 32 / kVec, kRowsAtOnce = 32 / kPieces;
     const int q = warp & 3;
-    TY *y = static_cast<TY *>(a.y);
-    uint32_t item = 0;
-    for (int64_t t = t0; t < n_tiles; t += dt, ++item) {
-      const Tile ti = tile(t);
+    TY *y = static_cast<TY *>(a.y), *turn = reinterpret_cast<TY *>(sm + S::kTurnOff) + q * 32 * 32;
+    const int piece = lane % kPieces, sub = lane / kPieces;
+    for (uint32_t item = 0; item < n_items; ++item) {
       const uint32_t acc = item % S::kAcc;
+      const Info *ti = tile(item);
+      if (ti == nullptr) break;
+      const int f = ti->f0 + (int)rank * kRowsA + q * 32 + piece * kVec, n = ti->rows;
       if (!mbar_wait_warp(&accf[acc], (item / S::kAcc) & 1, a.err, kErrProduct)) break;
       tc_after_sync();
-      const int f = ti.f0 + (int)rank * kRowsA + q * 32 + lane;
-      for (int c = 0; c < ti.rows; c += 32) {
-        const int row = c + lane < ti.rows ? a.sorted_rows[ti.first + c + lane] : 0;
+      for (int c = 0; c < n; c += 32) {
         float v[32];
         tmem_ld32_async(tmem + ((uint32_t)(q * 32) << 16) + acc * S::kTN + c, v);
         tmem_wait_ld();
-        const int m = min(32, ti.rows - c);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int64_t rj = __shfl_sync(0xffffffffu, row, j);
-          if (j < m && f < a.N) y[rj * a.ldy + f] = Elem<TY>::from_f(v[j]);
+        for (int j = 0; j < 32; ++j) turn[j * 32 + lane] = Elem<TY>::from_f(v[j]);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 32; j += kRowsAtOnce) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(turn + (j + sub) * 32 + piece * kVec);
+          if (c + j + sub < n && f < a.N) *reinterpret_cast<uint4 *>(y + (int64_t)ti->y[c + j + sub] * a.ldy + f) = u;
         }
+        __syncwarp();
       }
+      release(item);
       tc_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(leader_addr(&acce[acc]));
     }
-  } else if (warp >= kRowWarp && warp < kRowWarp + 4) {
-    // ---- x rows: this CTA's half of the tile's rows, a thread the same 16
-    // bytes of every 16th row of a stage
+  } else if (warp < kScaleWarp) {
+    // ---- x rows: this CTA's half of the tile's rows. Two groups of four warps
+    // take the stages in turn (a group needs about 640 clocks for 128 rows, an
+    // MMA stage 512); a thread copies the same 16 bytes of every 16th row.
     constexpr int kMine = S::kTN / 32;
-    const int tid = threadIdx.x - kRowWarp * 32, r0 = tid >> 3, chunk = tid & 7;
-    uint32_t it = 0;
-    bool ok = true;
-    for (int64_t t = t0; t < n_tiles && ok; t += dt) {
-      const Tile ti = tile(t);
-      const int half = ti.n_pad() / 2;
+    const int group = (warp - kRowWarp) >> 2, tid = threadIdx.x & 127, r0 = tid >> 3, chunk = tid & 7;
+    const uint32_t to = smem_addr(sm + kBytesA) + swz128(r0, chunk);  // 16 rows on: 2048 bytes
+    Stage<S::kStages> st;
+    bool odd = false, ok = true;
+    for (uint32_t item = 0; item < n_items && ok; ++item) {
+      const Info *ti = tile(item);
+      if (ti == nullptr) break;
+      const int half = ti->n_pad() / 2;
       const uint8_t *src[kMine];
 #pragma unroll
-      for (int i = 0; i < kMine; ++i)  // rows past the segment repeat its last one; their columns are not stored
-        src[i] = a.x + (int64_t)(a.sorted_rows[ti.first + min((int)rank * half + r0 + 16 * i, ti.rows - 1)] / a.x_div) * a.ldx + chunk * 16;
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const uint32_t s = it % S::kStages;
-        if (!mbar_wait_warp(&empty[s], ((it / S::kStages) & 1) ^ 1, a.err, kErrProduct)) { ok = false; break; }
-        unsigned char *st = sm + s * S::kStageBytes + kBytesA;
+      for (int i = 0; i < kMine; ++i)
+        src[i] = a.x + (int64_t)ti->x[min((int)rank * half + r0 + 16 * i, S::kTN - 1)] * a.ldx + chunk * 16;
+      release(item);
+      for (int kb = 0; kb < nkb; ++kb, st.next(), odd = !odd) {
+        if (odd != (group != 0)) continue;
+        if (!mbar_wait_warp(&empty[st.s], st.phase ^ 1, a.err, kErrProduct)) { ok = false; break; }
+        const uint32_t dst = to + st.s * S::kStageBytes;
         const int off = kb * kStepBytes;
         const bool in = off + chunk * 16 < row_bytes;
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int r = r0 + 16 * i;
-          if (r < half) cp_async16_zfill(st + swz128(r, chunk), in ? src[i] + off : a.x, in);
-        }
-        cp_async_arrive(&rows[s]);
+        for (int i = 0; i < kMine; ++i)
+          if (r0 + 16 * i < half) cp_async16_to(dst + 2048 * i, in ? src[i] + off : a.x, in);
+        cp_async_arrive(&rows[st.s]);
       }
     }
     cp_async_wait_upto(0);
-  } else if constexpr (S::kMx) if (warp >= kScaleWarp) {
-    // ---- scale bytes. The warps take chunks of 512 elements (16 bytes a
-    // row, two stages) in turn; lane l holds rows l, l + 32, ... of the weights
-    // and of x. Words land as [row % 32][row / 32 % 4] of a 512-byte atom.
-    uint32_t it = 0, chunk = 0;
+  } else if constexpr (S::kMx) {
+    // ---- scale bytes of the x rows. The warps take chunks of 512 elements (16
+    // bytes a row, two stages) in turn; lane l holds rows l, l + 32, ... Words
+    // land as [row % 32][row / 32 % 4] of a 512-byte atom, like the weights'
+    // tiles. A chunk is requested before the previous one is stored.
+    constexpr int kGb = S::kTN / 32;
     const int nb = a.K / LORA_MX_BLOCK;
+    struct Chunk { uint4 b[kGb]; };
+    uint32_t it = 0;
+    int skip = warp - kScaleWarp;  // chunks of the other warps before this warp's next
     bool ok = true;
-    for (int64_t t = t0; t < n_tiles && ok; t += dt, it += nkb) {
-      const Tile ti = tile(t);
-      constexpr int kGb = 4 * S::kAtomsB;
-      const uint8_t *pa[4], *pb[kGb];
+    for (uint32_t item = 0; item < n_items && ok; ++item, it += nkb) {
+      const Info *ti = tile(item);
+      if (ti == nullptr) break;
+      const int n = ti->rows;
+      int xr[kGb];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int f = min(ti.f0 + (int)rank * kRowsA + 32 * g + lane, a.N - 1);
-        pa[g] = a.W_scale + ((int64_t)(ti.slot - 1) * a.N + f) * a.ld_ws;
-      }
-#pragma unroll
-      for (int g = 0; g < kGb; ++g)
-        pb[g] = a.x_scale + (int64_t)(a.sorted_rows[ti.first + min(32 * g + lane, ti.rows - 1)] / a.x_div) * a.ld_xs;
-      for (int kb0 = 0; kb0 < nkb && ok; kb0 += 2, ++chunk) {
-        if (chunk % S::kScaleWarps != (uint32_t)(warp - kScaleWarp)) continue;
-        uint4 va[4], vb[kGb];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) va[g] = __ldg(reinterpret_cast<const uint4 *>(pa[g] + kb0 * 8));
+      for (int g = 0; g < kGb; ++g) xr[g] = ti->x[32 * g + lane];
+      release(item);
+      auto load = [&](Chunk &v, int kb) {
+        if (kb >= nkb) return;
 #pragma unroll
         for (int g = 0; g < kGb; ++g)
-          if (32 * g < ti.rows) vb[g] = __ldg(reinterpret_cast<const uint4 *>(pb[g] + kb0 * 8));
-          else vb[g] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+          if (32 * g < n) v.b[g] = __ldg(reinterpret_cast<const uint4 *>(a.x_scale + (int64_t)xr[g] * a.ld_xs + kb * 8));
+      };
+      Chunk now{}, then{};
+      int kb0 = 2 * skip;
+      load(now, kb0);
+      for (; kb0 < nkb && ok; kb0 += 2 * S::kScaleWarps) {
+        load(then, kb0 + 2 * S::kScaleWarps);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // the chunk's stages
           if (kb0 + h >= nkb) break;
           const uint32_t i = it + kb0 + h, s = i % S::kStages;
           if (!mbar_wait_warp(&empty[s], ((i / S::kStages) & 1) ^ 1, a.err, kErrProduct)) { ok = false; break; }
-          unsigned char *sf = sm + s * S::kStageBytes + kBytesA + S::kBytesB;
+          unsigned char *sf = sm + s * S::kStageBytes + kBytesA + S::kBytesB + 2 * kMxTileBytes;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             // Scales past the row's blocks stand beside codes the loads filled with
             // zeros; any number will do, a NaN would not.
             const int left = nb - ((kb0 + h) * 8 + 4 * w);
             const uint32_t keep = left >= 4 ? 0xffffffffu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-            auto word = [&](const uint4 &v) {
+            auto word = [&](int g) {
+              if (g >= kGb) return 0x7f7f7f7fu;
+              const uint4 &v = now.b[g < kGb ? g : 0];
               const uint32_t u = h == 0 ? (w == 0 ? v.x : v.y) : (w == 0 ? v.z : v.w);
               return (u & keep) | (0x7f7f7f7fu & ~keep);
             };
-            *reinterpret_cast<uint4 *>(sf + w * 512 + lane * 16) = make_uint4(word(va[0]), word(va[1]), word(va[2]), word(va[3]));
 #pragma unroll
             for (int b = 0; b < S::kAtomsB; ++b)
-              *reinterpret_cast<uint4 *>(sf + 1024 + (w * S::kAtomsB + b) * 512 + lane * 16) =
-                  make_uint4(word(vb[4 * b]), word(vb[4 * b + 1]), word(vb[4 * b + 2]), word(vb[4 * b + 3]));
+              *reinterpret_cast<uint4 *>(sf + (w * S::kAtomsB + b) * 512 + lane * 16) =
+                  make_uint4(word(4 * b), word(4 * b + 1), word(4 * b + 2), word(4 * b + 3));
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&rows[s]);
         }
+        now = then;
       }
+      skip = (kb0 - (nkb + 1) / 2 * 2) / 2;
     }
   }
   tc_before_sync();
@@ -435,14 +528,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
 
 // ------------------------------------------------------------------ host side
 
-cudaError_t encode(CUtensorMap *m, const void *base, bool mx, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+cudaError_t encode(CUtensorMap *m, const void *base, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
                    const cuuint32_t *box) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
   if (enc == nullptr) return cudaErrorNotSupported;
   const cuuint32_t es[3] = {1, 1, 1};
-  const CUresult r = enc(m, mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
-                         const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = enc(m, type, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -496,7 +588,7 @@ cudaError_t launch(const TcMaps &maps, const TcArgs &a, int num_tokens, int y_dt
 
 using NarrowBf16 = Shape<false, 64, 2, 10>;
 using WideBf16 = Shape<false, 256, 2, 6>;
-using NarrowMx = Shape<true, 64, 2, 9, 4>;
+using NarrowMx = Shape<true, 64, 2, 9, 2>;
 using WideMx = Shape<true, 192, 2, 5, 2>;
 
 }  // namespace
@@ -513,15 +605,23 @@ cudaError_t launch_moe_product_tc(const lora_expert_desc &d, const MetaView &mv,
   const cuuint64_t wd[3] = {elems, (cuuint64_t)d.d_out, (cuuint64_t)d.num_experts};
   const cuuint64_t ws[2] = {row_bytes, row_bytes * (cuuint64_t)d.d_out};
   const cuuint32_t wb[3] = {step, kRowsA, 1};
-  cudaError_t e = encode(&maps.W, d.W, mx, 3, wd, ws, wb);
+  cudaError_t e = encode(&maps.W, d.W, mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                         CU_TENSOR_MAP_SWIZZLE_128B, 3, wd, ws, wb);
   if (e != cudaSuccess) return e;
+  if (mx) {
+    const cuuint64_t sd[2] = {kMxTileBytes / 2, (cuuint64_t)d.num_experts * mx_tiles_out(d.d_out) * (mx_tiles_in(d.d_in) / 2)};
+    const cuuint64_t ss[1] = {2 * kMxTileBytes};
+    const cuuint32_t sb[2] = {kMxTileBytes / 2, 1};
+    e = encode(&maps.W_scale, d.W_scale, CU_TENSOR_MAP_DATA_TYPE_UINT32, CU_TENSOR_MAP_SWIZZLE_NONE, 2, sd, ss, sb);
+    if (e != cudaSuccess) return e;
+  } else {
+    maps.W_scale = maps.W;  // not used
+  }
   TcArgs a;
   a.x = static_cast<const uint8_t *>(x);
   a.ldx = mx ? ldx / 2 : ldx * 2;
   a.x_scale = x_scale;
-  a.W_scale = d.W_scale;
   a.ld_xs = ld_xs;
-  a.ld_ws = d.ld_scale;
   a.ldy = ldy;
   a.y = y;
   a.work = mv.work;

@@ -4,11 +4,19 @@
 // sits in the low four bits of byte i.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace ra {
 
 constexpr int kMxBlock = LORA_MX_BLOCK;
+
+// Tiles of an expert's scale bytes (lora_mx_tile_scales): 512 bytes for every
+// 128 outputs and 128 elements, an even number of them along the elements.
+constexpr int kMxTile = 128, kMxTileBytes = 512;
+__host__ __device__ constexpr int mx_tiles_out(int d_out) { return (d_out + kMxTile - 1) / kMxTile; }
+__host__ __device__ constexpr int mx_tiles_in(int d_in) { return (d_in + 2 * kMxTile - 1) / (2 * kMxTile) * 2; }
 
 // Eight elements to e2m1 codes, nearest (ties to the even code), magnitudes
 // above 6 saturate; element 0 in the lowest four bits.
@@ -25,11 +33,23 @@ __device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8]) {
   return r;
 }
 
-// The value of one code: sign, two exponent bits, one mantissa bit.
-__device__ __forceinline__ float mx_decode(uint32_t code) {
-  const uint32_t e = (code >> 1) & 3u, m = code & 1u;
-  const float mag = e == 0 ? 0.5f * (float)m : __uint_as_float(((e + 126u) << 23) | (m << 22));
-  return (code & 8u) ? -mag : mag;
+// The values of eight codes (lowest four bits first).
+__device__ __forceinline__ void mx_decode8(uint32_t q, float (&v)[8]) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(q));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
 }
 
 // 2^(b - 127); byte 0 is 2^-127 (subnormal), byte 255 NaN.

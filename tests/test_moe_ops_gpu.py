@@ -144,6 +144,18 @@ def test_mx_quantize_round_trip(lib, dt, rows, cols, pad):
         assert np.array_equal(f64(y), rv, equal_nan=True)
 
 
+@pytest.mark.parametrize("E,N,K,ld", [(1, 8, 32, 16), (3, 136, 288, 16), (2, 256, 4160, 144), (5, 40, 512, 32)])
+def test_mx_tile_scales(lib, E, N, K, ld):
+    s = torch.randint(0, 256, (E * N, ld), dtype=torch.uint8, device="cuda")
+    out = torch.full((lib.lora_mx_tiles_bytes(E, N, K),), 9, dtype=torch.uint8, device="cuda")
+    lib.check(lib.lora_mx_tile_scales(s.data_ptr(), ld, E, N, K, out.data_ptr()))
+    to, ti, nb = -(-N // 128), -(-K // 256) * 2, K // 32
+    want = np.full((E, to * 128, ti * 4), 127, np.uint8)
+    want[:, :N, :nb] = s.cpu().numpy().reshape(E, N, ld)[:, :, :nb]
+    want = want.reshape(E, to, 4, 32, ti, 4).transpose(0, 1, 4, 3, 2, 5)      # [e][out][in][row % 32][row / 32][block]
+    assert np.array_equal(out.cpu().numpy(), want.reshape(-1))
+
+
 # ----------------------------------------------------------------------------- products
 
 def slots_of(pattern, P, E, seed):

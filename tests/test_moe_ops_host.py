@@ -47,21 +47,21 @@ def _meta(ra, T=8, S=5):
 
 
 def test_product(ra):
-    def f(dt=ra.LORA_BF16, K=64, N=32, E=4, W=P, ws=0, lws=0, div=1, T=8, S=5, x=P, ldx=64, xs=0, lxs=0, y=P, ldy=32,
+    def f(dt=ra.LORA_BF16, K=64, N=32, E=4, W=P, ws=0, div=1, T=8, S=5, x=P, ldx=64, xs=0, lxs=0, y=P, ldy=32,
           ydt=ra.LORA_BF16, meta=True):
         d = ra.ExpertDesc()
-        d.dtype, d.d_in, d.d_out, d.num_experts, d.W, d.W_scale, d.ld_scale, d.x_row_div = dt, K, N, E, W, ws or None, lws, div
+        d.dtype, d.d_in, d.d_out, d.num_experts, d.W, d.W_scale, d.x_row_div = dt, K, N, E, W, ws or None, div
         return ra.lora_moe_product(d, _meta(ra, T, S), x, ldx, xs, lxs, y, ldy, ydt, 0)
-    mx = dict(dt=ra.LORA_MXFP4, ws=P, lws=16, xs=P, lxs=16)
+    mx = dict(dt=ra.LORA_MXFP4, ws=P, xs=P, lxs=16)
     assert f(T=0, x=0, y=0) == ra.LORA_OK and f(**{**mx, "T": 0}) == ra.LORA_OK
     for kw in (dict(dt=9), dict(K=0), dict(K=12), dict(N=0), dict(N=12), dict(div=-1), dict(W=0), dict(S=6), dict(x=0),
                dict(y=0), dict(ldx=56), dict(ldy=24), dict(ydt=ra.LORA_MXFP4), {**mx, "ws": 0}, {**mx, "xs": 0},
-               {**mx, "K": 40, "ldx": 64}, {**mx, "lws": 0}, {**mx, "lxs": 0}):
+               {**mx, "K": 40, "ldx": 64}, {**mx, "lxs": 0}):
         assert f(**kw) == ra.LORA_EINVAL, kw
     for kw in (dict(E=0, S=1), dict(E=1024, S=1025), dict(T=-1)):
         assert f(**kw) == ra.LORA_ERANGE, kw
     for kw in (dict(W=P + 8), dict(x=P + 8), dict(y=P + 2), dict(ldx=68), dict(ldy=36), {**mx, "ws": P + 8},
-               {**mx, "xs": P + 4}, {**mx, "lws": 24}, {**mx, "lxs": 20}, {**mx, "ldx": 80}):
+               {**mx, "xs": P + 4}, {**mx, "lxs": 20}, {**mx, "ldx": 80}):
         assert f(**kw) == ra.LORA_EALIGN, kw
     assert f(dt=ra.LORA_F32) == ra.LORA_EUNSUPPORTED
 
@@ -78,6 +78,20 @@ def test_mx(ra):
     assert f(rows=-1) == ra.LORA_ERANGE
     for kw in (dict(x=P + 2), dict(ldx=68), dict(c=P + 4), dict(ldc=40), dict(s=P + 1), dict(lds=24)):
         assert f(**kw) == ra.LORA_EALIGN, kw
+
+
+def test_tile_scales(ra):
+    def f(s=P, ld=16, E=3, N=40, K=96, t=P):
+        return ra.lora_mx_tile_scales(s, ld, E, N, K, t, 0)
+    for kw in (dict(E=0), dict(E=1024)):
+        assert f(**kw) == ra.LORA_ERANGE, kw
+    for kw in (dict(N=0), dict(N=12), dict(K=0), dict(K=40), dict(s=0), dict(t=0), dict(ld=0)):
+        assert f(**kw) == ra.LORA_EINVAL, kw
+    for kw in (dict(s=P + 8), dict(t=P + 4), dict(ld=24)):
+        assert f(**kw) == ra.LORA_EALIGN, kw
+    assert ra.lora_mx_tiles_bytes(3, 40, 96) == 3 * 1 * 2 * 512
+    assert ra.lora_mx_tiles_bytes(2, 129, 257) == 2 * 2 * 4 * 512
+    assert ra.lora_mx_tiles_bytes(0, 8, 32) == ra.lora_mx_tiles_bytes(1024, 8, 32) == ra.lora_mx_tiles_bytes(1, 0, 32) == 0
 
 
 def test_act(ra):
