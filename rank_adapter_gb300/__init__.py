@@ -161,9 +161,19 @@ def check(status: int, what: str = "") -> None:
         raise LoraError(status, what)
 
 
+_current = None  # (current raw stream of a device, current device), once torch has set CUDA up
+
+
 def _stream(stream) -> Optional[int]:
+    global _current
     if stream is None:
+        if _current is not None:
+            return _current[0](_current[1]())
         import torch
+        # torch.cuda.current_stream() takes 5 us a call, half of a small call's time on the host; the
+        # accessors below are what it wraps.
+        if torch.cuda.is_initialized() and hasattr(torch._C, "_cuda_getCurrentRawStream"):
+            _current = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
         return torch.cuda.current_stream().cuda_stream
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -226,33 +236,33 @@ def lora_moe_route(logits: int, ld_logits: int, dtype: int, num_tokens: int, num
                    renormalize: bool, scale: float, expert_map: int, local_experts: int, topk_ids: int, topk_w: int,
                    pair_slot: int, stream=None) -> int:
     """Router: topk experts of every token, their weights and (pair_slot) the pairs' product slots."""
-    return _lib.lora_moe_route(logits or None, ld_logits, dtype, num_tokens, num_experts, topk, score,
-                               int(bool(renormalize)), scale, expert_map or None, local_experts, topk_ids or None,
-                               topk_w or None, pair_slot or None, _stream(stream))
+    return _lib.lora_moe_route(logits, ld_logits, dtype, num_tokens, num_experts, topk, score,
+                               int(bool(renormalize)), scale, expert_map, local_experts, topk_ids,
+                               topk_w, pair_slot, _stream(stream))
 
 
 def lora_moe_product(desc: ExpertDesc, meta: Meta, x: int, ldx: int, x_scale: int, ld_xscale: int, y: int, ldy: int,
                      y_dtype: int, stream=None) -> int:
     """y[p] = x[p / x_row_div] . W[slot p - 1]^T for pairs with a slot (see the header)."""
-    return _lib.lora_moe_product(ctypes.byref(desc), ctypes.byref(meta), x or None, ldx, x_scale or None, ld_xscale,
-                                 y or None, ldy, y_dtype, _stream(stream))
+    return _lib.lora_moe_product(ctypes.byref(desc), ctypes.byref(meta), x, ldx, x_scale, ld_xscale,
+                                 y, ldy, y_dtype, _stream(stream))
 
 
 def lora_mx_quantize(x: int, ldx: int, x_dtype: int, rows: int, cols: int, codes: int, ld_codes: int, scales: int,
                      ld_scales: int, stream=None) -> int:
-    return _lib.lora_mx_quantize(x or None, ldx, x_dtype, rows, cols, codes or None, ld_codes, scales or None,
+    return _lib.lora_mx_quantize(x, ldx, x_dtype, rows, cols, codes, ld_codes, scales,
                                  ld_scales, _stream(stream))
 
 
 def lora_mx_dequantize(codes: int, ld_codes: int, scales: int, ld_scales: int, rows: int, cols: int, y: int, ldy: int,
                        y_dtype: int, stream=None) -> int:
-    return _lib.lora_mx_dequantize(codes or None, ld_codes, scales or None, ld_scales, rows, cols, y or None, ldy,
+    return _lib.lora_mx_dequantize(codes, ld_codes, scales, ld_scales, rows, cols, y, ldy,
                                    y_dtype, _stream(stream))
 
 
 def lora_mx_tile_scales(scales: int, ld_scales: int, num_experts: int, d_out: int, d_in: int, tiles: int,
                         stream=None) -> int:
-    return _lib.lora_mx_tile_scales(scales or None, ld_scales, num_experts, d_out, d_in, tiles or None, _stream(stream))
+    return _lib.lora_mx_tile_scales(scales, ld_scales, num_experts, d_out, d_in, tiles, _stream(stream))
 
 
 def lora_mx_tiles_bytes(num_experts: int, d_out: int, d_in: int) -> int:
@@ -261,20 +271,20 @@ def lora_mx_tiles_bytes(num_experts: int, d_out: int, d_in: int) -> int:
 
 def lora_moe_act(y13: int, ldy: int, y_dtype: int, pair_slot: int, num_pairs: int, inter: int, h: int, ldh: int,
                  h_dtype: int, stream=None) -> int:
-    return _lib.lora_moe_act(y13 or None, ldy, y_dtype, pair_slot or None, num_pairs, inter, h or None, ldh, h_dtype,
+    return _lib.lora_moe_act(y13, ldy, y_dtype, pair_slot, num_pairs, inter, h, ldh, h_dtype,
                              _stream(stream))
 
 
 def lora_moe_act_mx(y13: int, ldy: int, y_dtype: int, pair_slot: int, num_pairs: int, inter: int, codes: int,
                     ld_codes: int, scales: int, ld_scales: int, stream=None) -> int:
-    return _lib.lora_moe_act_mx(y13 or None, ldy, y_dtype, pair_slot or None, num_pairs, inter, codes or None, ld_codes,
-                                scales or None, ld_scales, _stream(stream))
+    return _lib.lora_moe_act_mx(y13, ldy, y_dtype, pair_slot, num_pairs, inter, codes, ld_codes,
+                                scales, ld_scales, _stream(stream))
 
 
 def lora_moe_combine(y: int, ldy: int, y_dtype: int, topk_w: int, pair_slot: int, num_tokens: int, topk: int, n: int,
                      out: int, ldo: int, out_dtype: int, accumulate: bool = False, stream=None) -> int:
-    return _lib.lora_moe_combine(y or None, ldy, y_dtype, topk_w or None, pair_slot or None, num_tokens, topk, n,
-                                 out or None, ldo, out_dtype, int(bool(accumulate)), _stream(stream))
+    return _lib.lora_moe_combine(y, ldy, y_dtype, topk_w, pair_slot, num_tokens, topk, n,
+                                 out, ldo, out_dtype, int(bool(accumulate)), _stream(stream))
 
 
 def lora_shrink_noalloc(desc: LayerDesc, meta: Meta, x: int, ldx: int, buf: int, stream=None) -> int:
@@ -493,33 +503,45 @@ def apply(table: SlotTable, meta: TokenMeta, x, y, buf=None, kind: int = LORA_AU
 
 # ----------------------------------------------------------------------------- the MoE layer around its LoRA
 
+_dtypes = {}
+
+
 def _dt(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return LORA_BF16
-    if t.dtype == torch.float32:
-        return LORA_F32
-    raise TypeError(f"expected a bf16 or fp32 tensor, got {t.dtype}")
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.bfloat16: LORA_BF16, torch.float32: LORA_F32})
+    d = _dtypes.get(t.dtype)
+    if d is None:
+        raise TypeError(f"expected a bf16 or fp32 tensor, got {t.dtype}")
+    return d
 
 
-def _rows(t, width: int, name: str, dtypes=None):
-    """(data pointer, row stride) of a 2-D tensor whose rows are contiguous and ``width`` wide."""
-    if t.dim() != 2 or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: expected [rows, {width}] with contiguous rows, got shape {tuple(t.shape)}, "
-                         f"strides {t.stride()}")
-    if dtypes is not None and t.dtype not in dtypes:
-        raise TypeError(f"{name}: {t.dtype}")
+def _rows(t, rows: int, width: int, name: str):
+    """(data pointer, row stride) of a 2-D tensor of at least ``rows`` contiguous rows, ``width`` wide."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != width or shape[0] < rows or (strides[1] != 1 and width > 1):
+        raise ValueError(f"{name}: expected [{rows}, {width}] with contiguous rows, got shape {tuple(shape)}, "
+                         f"strides {strides}")
+    if shape[0] > 1:
+        return t.data_ptr(), strides[0]
     # A single row's stride means nothing (torch may report any value): its length, rounded to the ABI's 16 bytes.
     es = t.element_size()
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else -(-width * es // 16) * 16 // es
+    return t.data_ptr(), -(-width * es // 16) * 16 // es
 
 
-def _vec(t, n: int, name: str, dtype):
-    """Data pointer of a contiguous tensor of n elements (0 for None)."""
+def _bytes(t, rows: int, width: Optional[int], name: str):
+    """_rows of a uint8 tensor (any width when None)."""
+    if t.element_size() != 1:
+        raise TypeError(f"{name}: expected uint8, got {t.dtype}")
+    return _rows(t, rows, t.shape[-1] if width is None else width, name)
+
+
+def _vec(t, n: int, name: str):
+    """Data pointer of a contiguous tensor of n 32-bit elements (0 for None)."""
     if t is None:
         return 0
-    if t.numel() != n or not t.is_contiguous() or t.dtype != dtype:
-        raise ValueError(f"{name}: expected {n} contiguous {dtype} elements, got {tuple(t.shape)} {t.dtype}")
+    if t.numel() != n or t.element_size() != 4 or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous 32-bit elements, got {tuple(t.shape)} {t.dtype}")
     return t.data_ptr()
 
 
@@ -573,17 +595,19 @@ def moe_route(logits, topk: int, score="softmax", renormalize: bool = True, scal
     """(topk_ids int32 [T, topk], topk_w fp32 [T, topk]) for logits [T, E] (see lora_moe_route).
 
     ``pair_slot`` (int32 [T * topk]): when given, also receives the pairs' product slots."""
-    import torch
-    T, E = int(logits.shape[0]), int(logits.shape[1])
-    lp, ld = _rows(logits, E, "logits")
-    if topk_ids is None:
-        topk_ids = torch.empty(T, topk, dtype=torch.int32, device=logits.device)
-    if topk_w is None:
-        topk_w = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
-    check(lora_moe_route(lp, max(ld, E), _dt(logits), T, E, topk, _SCORES.get(score, score), renormalize, scale,
-                         _vec(expert_map, E, "expert_map", torch.int32), E if local_experts is None else local_experts,
-                         _vec(topk_ids, T * topk, "topk_ids", torch.int32), _vec(topk_w, T * topk, "topk_w", torch.float32),
-                         _vec(pair_slot, T * topk, "pair_slot", torch.int32), stream), "lora_moe_route")
+    T, E = logits.shape
+    lp, ld = _rows(logits, T, E, "logits")
+    if topk_ids is None or topk_w is None:
+        import torch
+        if topk_ids is None:
+            topk_ids = torch.empty(T, topk, dtype=torch.int32, device=logits.device)
+        if topk_w is None:
+            topk_w = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
+    n = T * topk
+    check(_lib.lora_moe_route(lp, ld if ld > E else E, _dt(logits), T, E, topk, _SCORES.get(score, score), renormalize,
+                              scale, _vec(expert_map, E, "expert_map"), E if local_experts is None else local_experts,
+                              _vec(topk_ids, n, "topk_ids"), _vec(topk_w, n, "topk_w"), _vec(pair_slot, n, "pair_slot"),
+                              _stream(stream)), "lora_moe_route")
     return topk_ids, topk_w
 
 
@@ -593,21 +617,21 @@ def moe_product(experts: ExpertWeights, meta: TokenMeta, x, y, x_scale=None, str
     ``meta``: prepared over the pairs' product slots. x: [rows, d_in] of the weights' type; with 4-bit weights
     the codes [rows, d_in / 2] and ``x_scale`` [rows, ld] of mx4_quantize."""
     d, P = experts.desc, meta.c.num_tokens
-    mx = d.dtype == LORA_MXFP4
-    if not mx and _dt(x) != d.dtype or mx and (x.element_size() != 1 or x_scale is None):
-        raise TypeError(f"moe_product: x of {x.dtype} does not go with the experts' weights")
-    xp, ldx = _rows(x, d.d_in // 2 if mx else d.d_in, "x")
-    need = -(-P // max(1, d.x_row_div))
-    if x.shape[0] < need or y.shape[0] < P:
-        raise ValueError(f"moe_product: {P} pairs need {need} rows of x and {P} of y, got {x.shape[0]} and {y.shape[0]}")
-    sp, lds = 0, 0
-    if mx:
-        sp, lds = _rows(x_scale, x_scale.shape[1], "x_scale")
-        if x_scale.shape[0] < need:
-            raise ValueError(f"moe_product: {need} rows of x_scale needed, got {x_scale.shape[0]}")
+    rows, d_in = -(-P // max(1, d.x_row_div)), d.d_in
+    sp = lds = 0
+    if d.dtype == LORA_MXFP4:
+        if x_scale is None:
+            raise TypeError("moe_product: 4-bit weights take x as mx4_quantize gives it, with x_scale")
+        xp, ldx = _bytes(x, rows, d_in // 2, "x")
+        sp, lds = _bytes(x_scale, rows, None, "x_scale")
         ldx *= 2
-    yp, ldy = _rows(y, d.d_out, "y")
-    check(lora_moe_product(d, meta.c, xp, ldx, sp, lds, yp, ldy, _dt(y), stream), "lora_moe_product")
+    else:
+        if _dt(x) != d.dtype:
+            raise TypeError(f"moe_product: x of {x.dtype} does not go with the experts' weights")
+        xp, ldx = _rows(x, rows, d_in, "x")
+    yp, ldy = _rows(y, P, d.d_out, "y")
+    check(_lib.lora_moe_product(ctypes.byref(d), ctypes.byref(meta.c), xp, ldx, sp, lds, yp, ldy, _dt(y),
+                                _stream(stream)), "lora_moe_product")
 
 
 def mx4_buffers(rows: int, cols: int, device="cuda"):
@@ -619,68 +643,54 @@ def mx4_buffers(rows: int, cols: int, device="cuda"):
 
 def mx4_quantize(x, codes=None, scales=None, stream=None):
     """(codes, scales) of the rows of x [rows, cols] in the microscaled 4-bit format (see lora_mx_quantize)."""
-    rows, cols = int(x.shape[0]), int(x.shape[1])
+    rows, cols = x.shape
     if codes is None or scales is None:
         c, s = mx4_buffers(rows, cols, x.device)
         codes, scales = c if codes is None else codes, s if scales is None else scales
-    xp, ldx = _rows(x, cols, "x")
-    cp, ldc, sp, lds = _mx_ptrs(codes, scales, rows, cols)
-    check(lora_mx_quantize(xp, ldx, _dt(x), rows, cols, cp, ldc, sp, lds, stream), "lora_mx_quantize")
+    xp, ldx = _rows(x, rows, cols, "x")
+    cp, ldc = _bytes(codes, rows, cols // 2, "codes")
+    sp, lds = _bytes(scales, rows, None, "scales")
+    check(_lib.lora_mx_quantize(xp, ldx, _dt(x), rows, cols, cp, ldc, sp, lds, _stream(stream)), "lora_mx_quantize")
     return codes, scales
 
 
 def mx4_dequantize(codes, scales, y, stream=None):
     """y [rows, cols] = the values that codes and scales stand for (see lora_mx_dequantize)."""
-    rows, cols = int(y.shape[0]), int(y.shape[1])
-    yp, ldy = _rows(y, cols, "y")
-    cp, ldc, sp, lds = _mx_ptrs(codes, scales, rows, cols)
-    check(lora_mx_dequantize(cp, ldc, sp, lds, rows, cols, yp, ldy, _dt(y), stream), "lora_mx_dequantize")
+    rows, cols = y.shape
+    yp, ldy = _rows(y, rows, cols, "y")
+    cp, ldc = _bytes(codes, rows, cols // 2, "codes")
+    sp, lds = _bytes(scales, rows, None, "scales")
+    check(_lib.lora_mx_dequantize(cp, ldc, sp, lds, rows, cols, yp, ldy, _dt(y), _stream(stream)), "lora_mx_dequantize")
     return y
-
-
-def _mx_ptrs(codes, scales, rows: int, cols: int):
-    import torch
-    cp, ldc = _rows(codes, cols // 2, "codes", (torch.uint8,))
-    sp, lds = _rows(scales, scales.shape[1], "scales", (torch.uint8,))
-    if codes.shape[0] < rows or scales.shape[0] < rows:
-        raise ValueError(f"{rows} rows need as many of codes and scales, got {codes.shape[0]} and {scales.shape[0]}")
-    return cp, ldc, sp, lds
 
 
 def moe_act(y13, h, pair_slot=None, stream=None):
     """h[p] = silu(gate) * up of y13's rows [gate | up], for pairs with a slot (see lora_moe_act)."""
-    import torch
-    P, inter = int(h.shape[0]), int(h.shape[1])
-    yp, ldy = _rows(y13, 2 * inter, "y13")
-    if y13.shape[0] != P:
-        raise ValueError(f"moe_act: y13 has {y13.shape[0]} rows, h {P}")
-    hp, ldh = _rows(h, inter, "h")
-    check(lora_moe_act(yp, ldy, _dt(y13), _vec(pair_slot, P, "pair_slot", torch.int32), P, inter, hp, ldh, _dt(h),
-                       stream), "lora_moe_act")
+    P, inter = h.shape
+    yp, ldy = _rows(y13, P, 2 * inter, "y13")
+    hp, ldh = _rows(h, P, inter, "h")
+    check(_lib.lora_moe_act(yp, ldy, _dt(y13), _vec(pair_slot, P, "pair_slot"), P, inter, hp, ldh, _dt(h),
+                            _stream(stream)), "lora_moe_act")
     return h
 
 
 def moe_act_mx4(y13, codes, scales, pair_slot=None, stream=None):
     """moe_act into bf16, then mx4_quantize, in one pass (see lora_moe_act_mx)."""
-    import torch
-    P, inter = int(y13.shape[0]), int(y13.shape[1]) // 2
-    yp, ldy = _rows(y13, 2 * inter, "y13")
-    cp, ldc, sp, lds = _mx_ptrs(codes, scales, P, inter)
-    check(lora_moe_act_mx(yp, ldy, _dt(y13), _vec(pair_slot, P, "pair_slot", torch.int32), P, inter, cp, ldc, sp, lds,
-                          stream), "lora_moe_act_mx")
+    P, inter = y13.shape[0], y13.shape[1] // 2
+    yp, ldy = _rows(y13, P, 2 * inter, "y13")
+    cp, ldc = _bytes(codes, P, inter // 2, "codes")
+    sp, lds = _bytes(scales, P, None, "scales")
+    check(_lib.lora_moe_act_mx(yp, ldy, _dt(y13), _vec(pair_slot, P, "pair_slot"), P, inter, cp, ldc, sp, lds,
+                               _stream(stream)), "lora_moe_act_mx")
     return codes, scales
 
 
 def moe_combine(y, topk_w, out, pair_slot=None, accumulate: bool = False, stream=None):
     """out[t] (+)= sum_k topk_w[t, k] * y[t * topk + k] over the pairs with a slot (see lora_moe_combine)."""
-    import torch
-    T, topk, n = int(topk_w.shape[0]), int(topk_w.shape[1]), int(out.shape[1])
-    yp, ldy = _rows(y, n, "y")
-    op, ldo = _rows(out, n, "out")
-    if y.shape[0] != T * topk or out.shape[0] != T:
-        raise ValueError(f"moe_combine: {T} tokens of {topk} choices need {T * topk} rows of y and {T} of out, got "
-                         f"{y.shape[0]} and {out.shape[0]}")
-    check(lora_moe_combine(yp, ldy, _dt(y), _vec(topk_w, T * topk, "topk_w", torch.float32),
-                           _vec(pair_slot, T * topk, "pair_slot", torch.int32), T, topk, n, op, ldo, _dt(out),
-                           accumulate, stream), "lora_moe_combine")
+    (T, topk), n = topk_w.shape, out.shape[1]
+    yp, ldy = _rows(y, T * topk, n, "y")
+    op, ldo = _rows(out, T, n, "out")
+    check(_lib.lora_moe_combine(yp, ldy, _dt(y), _vec(topk_w, T * topk, "topk_w"),
+                                _vec(pair_slot, T * topk, "pair_slot"), T, topk, n, op, ldo, _dt(out), accumulate,
+                                _stream(stream)), "lora_moe_combine")
     return out
