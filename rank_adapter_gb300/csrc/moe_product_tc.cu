@@ -53,7 +53,7 @@ template <bool MX, int TN_, int ACC_, int STAGES_, int SW_ = 0>
 struct Shape {
   static constexpr bool kMx = MX;
   static constexpr int kTN = TN_, kAcc = ACC_, kStages = STAGES_;
-  static constexpr int kScaleWarps = SW_, kThreads = 32 * (kScaleWarp + kScaleWarps);
+  static constexpr int kScaleWarps = SW_, kThreads = 32 * (kScaleWarp + kScaleWarps + (MX ? 1 : 0));
   // A scale warp fills two stages in a row and skips those of the others. Its
   // wait tells a stage's phases apart only while its last own stage, 2 SW - 1
   // back, lies within one turn of the pipeline.
@@ -62,13 +62,12 @@ struct Shape {
   static constexpr int kAtomsB = (TN_ + 127) / 128;              // 512-byte scale atoms of a word of the x rows
   static constexpr int kBytesSf = MX ? 2 * (1 + kAtomsB) * 512 : 0;
   static constexpr int kStageBytes = kBytesA + kBytesB + kBytesSf;
-  // TMEM: the accumulators, then the scales of kSfSlots stages.
+  // TMEM: the accumulators, then each stage's scales.
   static constexpr int kSfCols = MX ? 8 + 8 * kAtomsB : 0, kSfCol = ACC_ * TN_;
-  static constexpr int kSfSlots = MX ? ((512 - kSfCol) / kSfCols < STAGES_ ? (512 - kSfCol) / kSfCols : STAGES_) : 0;
-  static constexpr int kUsedCols = kSfCol + kSfSlots * kSfCols;
+  static constexpr int kUsedCols = kSfCol + STAGES_ * kSfCols;
   static constexpr int kTmemCols = kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
-  static_assert(kUsedCols <= 512 && (!MX || kSfSlots >= 2), "TMEM");
-  static constexpr int kBarriers = 3 * STAGES_ + 2 * ACC_ + 2 * kRing + 1;
+  static_assert(kUsedCols <= 512, "TMEM");
+  static constexpr int kBarriers = 4 * STAGES_ + 2 * ACC_ + 2 * kRing + 1;
   static constexpr int kTurnOff = STAGES_ * kStageBytes;         // the epilogue warps' 32 x 32 blocks
   static constexpr int kRingOff = kTurnOff + 4 * 32 * 32 * 4;
   static constexpr int kBarOff = kRingOff + kRing * (int)sizeof(TileInfo<TN_>);
@@ -130,6 +129,13 @@ __device__ __forceinline__ void mma_commit2(uint64_t *bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t.reg .b16 m;\n\telect.sync r|e, 0xffffffff;\n\tmov.b16 m, 3;\n\t"
       "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}"
+      ::"r"(smem_addr(bar)) : "memory");
+}
+// One arrival on the leader's barrier once every tensor-core copy issued so far is complete.
+__device__ __forceinline__ void commit2_leader(uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
       ::"r"(smem_addr(bar)) : "memory");
 }
 // The four MMAs of a stage (32 bytes of each row a step), one elected lane.
@@ -207,7 +213,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
   uint64_t *full = reinterpret_cast<uint64_t *>(sm + S::kBarOff);  // leader's: a stage of both CTAs is in
   uint64_t *empty = full + S::kStages;  // the stage's MMAs are done
   uint64_t *rows = empty + S::kStages;  // this CTA's x rows (and scales) of a stage are in
-  uint64_t *accf = rows + S::kStages;   // an accumulator is complete
+  uint64_t *sfull = rows + S::kStages;  // leader's: a stage's scales are in TMEM (4-bit)
+  uint64_t *accf = sfull + S::kStages;  // an accumulator is complete
   uint64_t *acce = accf + S::kAcc;      // leader's: both CTAs have read it
   uint64_t *tfull = acce + S::kAcc;     // a tile is described
   uint64_t *tempty = tfull + kRing;     // every warp has what it needs of it
@@ -220,6 +227,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&full[s], 3);  // the weights' bytes, and each CTA's rows
       mbar_init(&empty[s], 1);
+      mbar_init(&sfull[s], 1);
       mbar_init(&rows[s], 128 + (S::kMx ? 1 : 0));
     }
     for (int i = 0; i < S::kAcc; ++i) {
@@ -313,7 +321,6 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
     // ---- MMA issue (leader)
     if (rank == 0) {
       Stage<S::kStages> st;
-      uint32_t it = 0;
       bool ok = true;
       for (uint32_t item = 0; item < n_items && ok; ++item) {
         const Info *ti = tile(item);
@@ -323,28 +330,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
         const uint32_t acc = item % S::kAcc, d = tmem + acc * S::kTN;
         if (!mbar_wait_warp(&acce[acc], ((item / S::kAcc) & 1) ^ 1, a.err, kErrProduct)) break;
         tc_after_sync();
-        for (int kb = 0; kb < nkb; ++kb, ++it, st.next()) {
-          if (!mbar_wait_warp(&full[st.s], st.phase, a.err, kErrProduct)) { ok = false; break; }
-          if constexpr (S::kSfSlots < S::kStages && S::kMx)
-            // The scales of kSfSlots stages are in TMEM; a slot is free once the
-            // MMAs that many stages back are done.
-            if (it >= (uint32_t)S::kSfSlots) {
-              const uint32_t was = it - S::kSfSlots;
-              if (!mbar_wait_warp(&empty[was % S::kStages], (was / S::kStages) & 1, a.err, kErrProduct)) { ok = false; break; }
-            }
+        for (int kb = 0; kb < nkb; ++kb, st.next()) {
+          if (!mbar_wait_warp(S::kMx ? &sfull[st.s] : &full[st.s], st.phase, a.err, kErrProduct)) { ok = false; break; }
           tc_after_sync();
           const uint32_t at = smem_addr(sm + st.s * S::kStageBytes);
           const uint64_t ad = smem_desc(at, 16, 1024, kSw128), bd = smem_desc(at + kBytesA, 16, 1024, kSw128);
           if constexpr (S::kMx) {
-            const uint32_t sf = at + kBytesA + S::kBytesB;
-            const uint32_t sa = tmem + S::kSfCol + it % S::kSfSlots * S::kSfCols, sb = sa + 8;
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              scales_to_tmem(sa + 4 * w, smem_desc(sf + w * 512, 16, 128, 0));
-#pragma unroll
-              for (int h = 0; h < S::kAtomsB; ++h)
-                scales_to_tmem(sb + 4 * (w * S::kAtomsB + h), smem_desc(sf + 1024 + (w * S::kAtomsB + h) * 512, 16, 128, 0));
-            }
+            const uint32_t sa = tmem + S::kSfCol + st.s * S::kSfCols, sb = sa + 8;
             mma_stage_mx(d, ad, bd, idesc_mx(n, 0), idesc_mx(n, 2), sa, sa + 4, sb, sb + 4 * S::kAtomsB, kb > 0);
           } else {
             mma_stage_bf16(d, ad, bd, idesc_bf16_kk(n), kb > 0);
@@ -457,6 +449,23 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
       }
     }
     cp_async_wait_upto(0);
+  } else if (S::kMx && warp == kScaleWarp + S::kScaleWarps) {
+    // ---- scales of a stage to TMEM (leader). A warp of its own: with these
+    // copies in the MMA warp's stream its issue bound the kernel (w13 prefill
+    // 421 us, now 377 us).
+    if (rank == 0) {
+      Stage<S::kStages> st;
+      const uint64_t n = (uint64_t)n_items * nkb;
+      for (uint64_t i = 0; i < n; ++i, st.next()) {
+        if (!mbar_wait_warp(&full[st.s], st.phase, a.err, kErrProduct)) break;
+        tc_after_sync();
+        const uint32_t sf = smem_addr(sm + st.s * S::kStageBytes) + kBytesA + S::kBytesB;
+        const uint32_t sa = tmem + S::kSfCol + st.s * S::kSfCols;
+#pragma unroll
+        for (int w = 0; w < 2 * (1 + S::kAtomsB); ++w) scales_to_tmem(sa + 4 * w, smem_desc(sf + w * 512, 16, 128, 0));
+        commit2_leader(&sfull[st.s]);
+      }
+    }
   } else if constexpr (S::kMx) {
     // ---- scale bytes of the x rows. The warps take chunks of 512 elements (16
     // bytes a row, two stages) in turn; lane l holds rows l, l + 32, ... Words
