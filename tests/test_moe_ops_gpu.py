@@ -443,3 +443,45 @@ def test_nothing_to_do(lib):
     lib.moe_act(torch.empty(0, 64, device="cuda"), torch.empty(0, 32, device="cuda"))
     lib.moe_combine(torch.empty(0, 8, device="cuda"), torch.empty(0, 2, device="cuda"), torch.empty(0, 8, device="cuda"))
     assert lib.lora_launch_count() == n0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "mx4"])
+def test_offsets_past_32_bits(lib, dt):
+    """Rows of y and of x more than 2^31 elements from the start, weights more than 2^32 bytes."""
+    P, K, N, ld = 300000, 64, 8, 8192
+    y = torch.zeros(P, ld, dtype=torch.bfloat16, device="cuda")[:, :N]
+    x = torch.zeros(P, ld if dt == "bf16" else 16 * ld, dtype=torch.bfloat16 if dt == "bf16" else torch.uint8, device="cuda")
+    slot = torch.zeros(P, dtype=torch.int32, device="cuda")
+    pick = torch.tensor([0, 1, 262144, 270000, P - 1], device="cuda")
+    slot[pick] = 1
+    xr = torch.randint(-3, 4, (5, K), device="cuda").float()
+    W = torch.randint(-3, 4, (N, K), device="cuda").float()
+    meta = lib.TokenMeta(P, 2)
+    meta.prepare(slot)
+    if dt == "bf16":
+        x[pick, :K] = xr.bfloat16()
+        lib.moe_product(lib.ExpertWeights(W.bfloat16()[None].contiguous()), meta, x[:, :K], y)
+    else:
+        c, s = lib.mx4_quantize(xr)
+        x[pick, :K // 2] = c
+        xs = torch.zeros(P, s.shape[1], dtype=torch.uint8, device="cuda")
+        xs[pick] = s
+        wc, wsc = lib.mx4_quantize(W)
+        xr = lib.mx4_dequantize(c, s, torch.empty_like(xr))
+        W = lib.mx4_dequantize(wc, wsc, torch.empty_like(W))
+        lib.moe_product(lib.ExpertWeights(wc[None], wsc[None]), meta, x[:, :K // 2], y, x_scale=xs)
+    torch.cuda.synchronize()
+    ref = f64(xr) @ f64(W).T
+    assert (np.abs(f64(y[pick]) - ref) <= 2.0 ** -8 * np.abs(ref)).all()
+    assert int((y != 0).any(1).sum()) <= 5
+    if dt == "bf16":                                   # an expert whose weights start past 2^32 bytes
+        del x, y
+        E, Nw, Kw = 40, 8192, 8192
+        Wb = torch.zeros(E, Nw, Kw, dtype=torch.bfloat16, device="cuda")
+        Wb[E - 1] = torch.randint(-3, 4, (Nw, Kw), device="cuda").bfloat16()
+        xb = torch.randint(-3, 4, (3, Kw), device="cuda").bfloat16()
+        yb = torch.empty(3, Nw, device="cuda")
+        meta = lib.TokenMeta(3, E + 1)
+        meta.prepare(torch.full((3,), E, dtype=torch.int32, device="cuda"))
+        lib.moe_product(lib.ExpertWeights(Wb), meta, xb, yb)
+        assert np.array_equal(f64(yb), f64(xb) @ f64(Wb[E - 1]).T)
