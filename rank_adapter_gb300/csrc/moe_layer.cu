@@ -15,8 +15,9 @@ namespace {
 // and nothing is sorted that is not asked for. Lane k keeps choice k and the
 // weights need one or two warp sums. A long batch is bound by the rounds'
 // instructions: 16-bit logits carry their expert in the key's low half, so
-// that one reduction a round gives both (16381 tokens of 256 experts, top 8:
-// 11.5 us; with separate reductions, as for fp32 logits, 15.1 us).
+// that one reduction a round gives both, and lanes with few keys sort them first
+// (16381 tokens of 256 experts, top 8: 8.8 us;
+// unsorted 11.5 us; with separate reductions, as for fp32 logits, 15.1 us).
 
 constexpr int kRouteWarps = 4;
 
@@ -78,6 +79,32 @@ template <int NV> struct RouteKeys<__nv_bfloat16, NV> {
     return key_value(k >> 31 ? k & 0xffff0000u : k | 0xffffu);
   }
   __device__ __forceinline__ static bool numbered(uint32_t k) { return k >= (order_key(-INFINITY) | 0xffffu) + 1u; }
+  // The lane's keys largest first: Batcher's odd-even merge sort.
+  __device__ __forceinline__ void sort() {
+#pragma unroll
+    for (int p = 1; p < NV; p *= 2)
+#pragma unroll
+      for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+        for (int j = k % p; j + k < NV; j += 2 * k)
+#pragma unroll
+          for (int i = 0; i < k; ++i)
+            if (i + j + k < NV && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+              const uint32_t x = key[i + j], y = key[i + j + k];
+              key[i + j] = max(x, y);
+              key[i + j + k] = min(x, y);
+            }
+  }
+  __device__ __forceinline__ uint32_t take_sorted(int, int &e) {
+    const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
+    if (key[0] == best) {
+#pragma unroll
+      for (int i = 0; i + 1 < NV; ++i) key[i] = key[i + 1];
+      key[NV - 1] = 0u;
+    }
+    e = 0xffff - (int)(best & 0xffffu);
+    return best;
+  }
   __device__ __forceinline__ uint32_t take(int, int &e) {
     uint32_t m = key[0];
 #pragma unroll
@@ -99,6 +126,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(RouteArgs a
   const int lane = threadIdx.x & 31;
   constexpr uint32_t kAll = 0xffffffffu;
   using Keys = RouteKeys<T, NV>;
+  // A sorted lane offers its first key and moves up, an unsorted one searches
+  // all NV. Eight keys' sort is repaid from three rounds on (7.56 us, unsorted
+  // 7.87); sixteen keys' is not with eight (28.2 us, unsorted 21.7).
+  constexpr bool kSort = sizeof(T) == 2 && NV > 1 && NV <= 8;
   for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5); t < a.T;
        t += (int64_t)gridDim.x * kRouteWarps) {
     const T *row = static_cast<const T *>(a.logits) + t * a.ldl;
@@ -125,13 +156,26 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(RouteArgs a
     }
     uint32_t mine = 0, first = 0;  // keys of choice `lane` and of the first
     int id = 0;
-    for (int c = 0; c < a.topk; ++c) {
-      int e;
-      const uint32_t best = k.take(lane, e);
-      if (c == 0) first = best;
+    auto chose = [&](int c, uint32_t key, int e) {
+      if (c == 0) first = key;
       if (lane == c) {
-        mine = best;
+        mine = key;
         id = e;
+      }
+    };
+    int e;
+    if (kSort && a.topk >= 3) {
+      if constexpr (kSort) {
+        k.sort();
+        for (int c = 0; c < a.topk; ++c) {
+          const uint32_t key = k.take_sorted(lane, e);
+          chose(c, key, e);
+        }
+      }
+    } else {
+      for (int c = 0; c < a.topk; ++c) {
+        const uint32_t key = k.take(lane, e);
+        chose(c, key, e);
       }
     }
     const bool chosen = lane < a.topk, live = chosen && Keys::numbered(mine);
@@ -189,21 +233,49 @@ struct ActArgs {
 // (together within |g| * 2^-23 of the value, 2^-9 is rounded away; below -87,
 // where the value is under 1e-35, it may come out as 0); an fp32 result takes
 // the exact ones. At 32744 rows of 2048 the exact ones bind the kernel by
-// instructions (85.1 us, with the fast ones 67.3 us, 0.89 of the measured copy rate; more rows
-// a thread at once changed nothing).
+// instructions (88.5 us where the fast ones take 66.9).
 template <bool kFast> __device__ __forceinline__ float silu(float g) {
   if constexpr (kFast) return __fdividef(g, 1.f + __expf(-g));
   else return g / (1.f + expf(-g));
 }
 
-template <bool kFast, typename TY>
-__device__ __forceinline__ void act8(const ActArgs &a, int64_t p, int c, float (&v)[8]) {
-  const TY *row = static_cast<const TY *>(a.y13) + p * a.ldy + (int64_t)c * 8;
-  float u[8];
-  load8_f32(row, v);
-  load8_f32(row + a.inter, u);
+// The activation of chunk c of kActRows rows, p0 and every blockDim.y on: their
+// slots, then all their loads, then row by row the arithmetic and
+// put(p, live, v); live: the row is in range and has an expert. At 32744 rows
+// of 2048, one row a thread at a time 77.6 us, two 69.7 us, four 63.8 us
+// (0.94 of the measured copy rate).
+constexpr int kActRows = 4;
+
+template <bool kFast, typename TY, typename Put>
+__device__ __forceinline__ void act_rows(const ActArgs &a, int64_t p0, int c, bool in, Put put) {
+  int slot[kActRows];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = silu<kFast>(v[j]) * u[j];
+  for (int i = 0; i < kActRows; ++i) slot[i] = 1;
+  if (a.pair_slot != nullptr)
+#pragma unroll
+    for (int i = 0; i < kActRows; ++i)
+      slot[i] = __ldg(a.pair_slot + min(p0 + i * (int64_t)blockDim.y, (int64_t)a.P - 1));
+  Raw8<TY> g[kActRows], u[kActRows];
+#pragma unroll
+  for (int i = 0; i < kActRows; ++i) {
+    const int64_t p = p0 + i * blockDim.y;
+    if (!in || p >= a.P) slot[i] = 0;
+    const TY *row = static_cast<const TY *>(a.y13) + p * a.ldy + (int64_t)c * 8;
+    g[i] = u[i] = Raw8<TY>{};
+    if (slot[i] > 0) {
+      g[i] = raw8(row);
+      u[i] = raw8(row + a.inter);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kActRows; ++i) {
+    float v[8], w[8];
+    widen8(g[i], v);
+    widen8(u[i], w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = silu<kFast>(v[j]) * w[j];
+    put(p0 + i * blockDim.y, slot[i] > 0, v);
+  }
 }
 
 template <typename TY, typename TH>
@@ -212,12 +284,11 @@ __global__ void __launch_bounds__(kThreads) moe_act_kernel(ActArgs a) {
   pdl_trigger();
   const int c = blockIdx.x * blockDim.x + threadIdx.x;
   if (c >= a.inter / 8) return;
-  for (int64_t p = (int64_t)blockIdx.y * blockDim.y + threadIdx.y; p < a.P; p += (int64_t)gridDim.y * blockDim.y) {
-    if (a.pair_slot != nullptr && a.pair_slot[p] <= 0) continue;
-    float v[8];
-    act8<sizeof(TH) == 2, TY>(a, p, c, v);
-    store8(static_cast<TH *>(a.h) + p * a.ldh + (int64_t)c * 8, v);
-  }
+  const int64_t step = (int64_t)gridDim.y * blockDim.y * kActRows;
+  for (int64_t p0 = (int64_t)blockIdx.y * blockDim.y * kActRows + threadIdx.y; p0 < a.P; p0 += step)
+    act_rows<sizeof(TH) == 2, TY>(a, p0, c, true, [&](int64_t p, bool live, const float(&v)[8]) {
+      if (live) store8(static_cast<TH *>(a.h) + p * a.ldh + (int64_t)c * 8, v);
+    });
 }
 
 // The same into the 4-bit format. The activation is rounded to bf16 first, so
@@ -228,21 +299,20 @@ __global__ void __launch_bounds__(kThreads) moe_act_mx_kernel(ActArgs a) {
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x * blockDim.x + threadIdx.x;
-  for (int64_t p0 = (int64_t)blockIdx.y * blockDim.y; p0 < a.P; p0 += (int64_t)gridDim.y * blockDim.y) {
-    const int64_t p = p0 + threadIdx.y;
-    // The four lanes of a block of 32 are in one row and in range together.
-    const bool in = p < a.P && c < a.inter / 8 && (a.pair_slot == nullptr || a.pair_slot[p] > 0);
-    float v[8] = {};
-    if (in) act8<true, TY>(a, p, c, v);
+  const int64_t step = (int64_t)gridDim.y * blockDim.y * kActRows;
+  for (int64_t b0 = (int64_t)blockIdx.y * blockDim.y * kActRows; b0 < a.P; b0 += step)
+    act_rows<true, TY>(a, b0 + threadIdx.y, c, c < a.inter / 8, [&](int64_t p, bool live, const float(&v)[8]) {
+      // The four lanes of a block of 32 are in one row and in range together.
+      float r[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __bfloat162float(__float2bfloat16_rn(v[j]));
-    uint32_t byte;
-    const uint32_t q = mx_quantize8(v, byte);
-    if (in) {
-      *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.h) + p * a.ldh + (int64_t)c * 4) = q;
-      if ((c & 3) == 0) a.scales[p * a.lds + (c >> 2)] = (uint8_t)byte;
-    }
-  }
+      for (int j = 0; j < 8; ++j) r[j] = __bfloat162float(__float2bfloat16_rn(v[j]));
+      uint32_t byte;
+      const uint32_t q = mx_quantize8(r, byte);
+      if (live) {
+        *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.h) + p * a.ldh + (int64_t)c * 4) = q;
+        if ((c & 3) == 0) a.scales[p * a.lds + (c >> 2)] = (uint8_t)byte;
+      }
+    });
 }
 
 // ------------------------------------------------------------------ weighted sum
@@ -320,7 +390,7 @@ cudaError_t launch_moe_route(const void *logits, int64_t ldl, int dtype, int T, 
 cudaError_t launch_moe_act(const void *y13, int64_t ldy, int y_dtype, const int32_t *pair_slot, int P, int inter,
                            void *h, int64_t ldh, int h_dtype, cudaStream_t st) {
   const ActArgs a{y13, ldy, pair_slot, h, ldh, nullptr, 0, P, inter};
-  const RowGrid l = RowGrid::of(P, inter / 8, kThreads, 1);
+  const RowGrid l = RowGrid::of(P, inter / 8, kThreads, kActRows);
   void (*k)(ActArgs) =
       y_dtype == LORA_BF16
           ? (h_dtype == LORA_BF16 ? moe_act_kernel<__nv_bfloat16, __nv_bfloat16> : moe_act_kernel<__nv_bfloat16, float>)
@@ -331,7 +401,7 @@ cudaError_t launch_moe_act(const void *y13, int64_t ldy, int y_dtype, const int3
 cudaError_t launch_moe_act_mx(const void *y13, int64_t ldy, int y_dtype, const int32_t *pair_slot, int P, int inter,
                               uint8_t *codes, int64_t ldc, uint8_t *scales, int64_t lds, cudaStream_t st) {
   const ActArgs a{y13, ldy, pair_slot, codes, ldc, scales, lds, P, inter};
-  const RowGrid l = RowGrid::of(P, inter / 8, kThreads, 1);
+  const RowGrid l = RowGrid::of(P, inter / 8, kThreads, kActRows);
   return launch_pdl(y_dtype == LORA_BF16 ? moe_act_mx_kernel<__nv_bfloat16> : moe_act_mx_kernel<float>, l.grid, l.block,
                     0, st, 1u, a);
 }
