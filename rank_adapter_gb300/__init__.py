@@ -13,6 +13,10 @@ Low-level functions carry the C names and return the C status codes
 ``lora_last_cuda_error``). ``SlotTable`` and ``TokenMeta`` own torch buffers
 laid out as the ABI wants and call those functions; ``shrink`` / ``expand``
 raise ``LoraError`` on a non-zero status.
+
+The mixture-of-experts layer around its LoRA: ``moe_route``, ``ExpertWeights`` and
+``moe_product``, ``mx4_quantize`` / ``mx4_dequantize``, ``moe_act`` / ``moe_act_mx4`` and
+``moe_combine`` (``lora_moe_*`` and ``lora_mx_*`` in the header).
 """
 from __future__ import annotations
 

@@ -319,7 +319,11 @@ __global__ void __launch_bounds__(kThreads) moe_act_mx_kernel(ActArgs a) {
 //
 // out[t] = (out[t] or 0) + sum_k w[t, k] * y[t * topk + k], in fp32 in the
 // order of k and rounded once. A thread owns eight columns of a token; the
-// rows of up to kAhead choices are requested before the first is used.
+// rows of up to kAhead choices are requested before the first is used. With
+// tokens enough for every SM a CTA walks all columns of its tokens, so that
+// the token's slots and weights come from L1 after the first (32744 rows of
+// 7168: 85.4 us, 0.93 of the measured copy rate; with a CTA for each 2048
+// columns 94.8 us).
 
 struct CombineArgs {
   const void *y;
@@ -410,7 +414,8 @@ cudaError_t launch_moe_combine(const void *y, int64_t ldy, int y_dtype, const fl
                                int topk, int n, void *out, int64_t ldo, int out_dtype, int accumulate,
                                cudaStream_t st) {
   const CombineArgs a{y, ldy, w, pair_slot, out, ldo, T, topk, n, accumulate};
-  const RowGrid l = RowGrid::of(T, n / 8, kThreads, 1);
+  RowGrid l = RowGrid::of(T, n / 8, kThreads, 1);
+  if (T >= 152 * 8) l.grid.x = 1;
   void (*k)(CombineArgs) = y_dtype == LORA_BF16
                                ? (out_dtype == LORA_BF16 ? moe_combine_kernel<__nv_bfloat16, __nv_bfloat16>
                                                          : moe_combine_kernel<__nv_bfloat16, float>)

@@ -298,10 +298,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
         if (!mbar_wait_warp(&empty[st.s], st.phase ^ 1, a.err, kErrProduct)) { ok = false; break; }
         if (lane == 0) {
           if (rank == 0) mbar_arrive_tx(&full[st.s], 2 * (kBytesA + (S::kMx ? 2 * kMxTileBytes : 0)));
-          if constexpr (S::kMx)
-            tma_scales(smem_addr(sm + st.s * S::kStageBytes + kBytesA + S::kBytesB), &maps.W_scale, sf + kb, leader_addr(&full[st.s]));
           tma_w(smem_addr(sm + st.s * S::kStageBytes), &maps.W, kb * kElemsPerStep, f, e, leader_addr(&full[st.s]));
         }
+        if (S::kMx && lane == 1)
+          tma_scales(smem_addr(sm + st.s * S::kStageBytes + kBytesA + S::kBytesB), &maps.W_scale, sf + kb, leader_addr(&full[st.s]));
         __syncwarp();
       }
     }

@@ -45,7 +45,8 @@ def route_ref(z, topk, score, renorm, scale):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("T,E,topk,dt", [(1, 256, 8, "f32"), (1, 1, 1, "bf16"), (7, 33, 32, "f32"), (513, 64, 6, "bf16"),
-                                         (130, 1000, 8, "f32"), (65, 384, 1, "bf16"), (300, 8, 2, "f32"), (9, 512, 5, "bf16")])
+                                         (130, 1000, 8, "f32"), (65, 384, 1, "bf16"), (300, 8, 2, "f32"), (9, 512, 5, "bf16"),
+                                         (200, 256, 8, "bf16"), (64, 100, 3, "bf16"), (33, 40, 2, "bf16")])
 def test_route(lib, score, renorm, T, E, topk, dt):
     g = torch.Generator(device="cuda").manual_seed(T * 1000 + E)
     wide = torch.full((T, E + 3), 50.0, device="cuda", dtype=DT[dt])      # columns past E must not be seen
@@ -345,7 +346,7 @@ def test_act_mx4_is_act_then_quantize(lib, ydt, P, inter):
 
 
 @pytest.mark.parametrize("ydt,odt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
-@pytest.mark.parametrize("T,topk,n,acc,pad", [(1, 8, 7168, False, 0), (1, 1, 8, True, 0), (37, 6, 1000, True, 8),
+@pytest.mark.parametrize("T,topk,n,acc,pad", [(1, 8, 7168, False, 0), (1, 1, 8, True, 0), (1300, 8, 2056, False, 0), (37, 6, 1000, True, 8),
                                               (70000, 2, 16, False, 0), (64, 33, 136, False, 24), (300, 9, 264, True, 0)])
 def test_combine(lib, ydt, odt, T, topk, n, acc, pad):
     g = torch.Generator(device="cuda").manual_seed(T + n)
