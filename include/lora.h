@@ -415,7 +415,8 @@ typedef struct {
  *   x:    device, [ceil(num_tokens / x_row_div), d_in], row stride ldx
  *         elements, of desc->dtype (LORA_MXFP4: rows of codes, ldx / 2 bytes
  *         apart, with x_scale rows of ld_xscale bytes)
- *   y:    device, [num_tokens, d_out], row stride ldy, LORA_F32 or LORA_BF16
+ *   y:    device, [num_tokens, d_out], row stride ldy, LORA_F32 or LORA_BF16;
+ *         must not overlap x
  * Errors: null pointers, ldx < d_in, ldy < d_out, a slot count that differs,
  * ld_xscale too small -> LORA_EINVAL; an fp32 table with a bf16 y ->
  * LORA_EUNSUPPORTED; a pointer or row stride that is not a multiple of 16
@@ -446,7 +447,7 @@ int lora_mx_quantize(const void *x, int64_t ldx, int32_t x_dtype, int64_t rows, 
                      int64_t ld_codes, uint8_t *scales, int64_t ld_scales, lora_stream_t stream);
 
 /* The values that codes and scales stand for, y[r, c] = code * 2^(byte - 127)
- * (exact in LORA_F32 and LORA_BF16; byte 255 gives NaN). Arguments and errors
+ * (exact in LORA_F32 and LORA_BF16 up to the type's range; byte 255 gives NaN). Arguments and errors
  * as lora_mx_quantize. */
 int lora_mx_dequantize(const uint8_t *codes, int64_t ld_codes, const uint8_t *scales, int64_t ld_scales, int64_t rows,
                        int32_t cols, void *y, int64_t ldy, int32_t y_dtype, lora_stream_t stream);

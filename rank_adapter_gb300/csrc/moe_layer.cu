@@ -322,8 +322,9 @@ __global__ void __launch_bounds__(kThreads) moe_act_mx_kernel(ActArgs a) {
 // rows of up to kAhead choices are requested before the first is used. With
 // tokens enough for every SM a CTA walks all columns of its tokens, so that
 // the token's slots and weights come from L1 after the first (32744 rows of
-// 7168: 85.4 us, 0.93 of the measured copy rate; with a CTA for each 2048
-// columns 94.8 us).
+// 7168: 84.0 us, 0.94 of the measured copy rate; with CTAs of 256 threads 85.4
+// us, and with one of those for each 2048 columns 94.8 us).
+constexpr int kCombineThreads = 128;
 
 struct CombineArgs {
   const void *y;
@@ -337,7 +338,7 @@ struct CombineArgs {
 };
 
 template <typename TY, typename TO>
-__global__ void __launch_bounds__(kThreads, 4) moe_combine_kernel(CombineArgs a) {
+__global__ void __launch_bounds__(kCombineThreads, 8) moe_combine_kernel(CombineArgs a) {
   pdl_wait();
   pdl_trigger();
   constexpr int kAhead = sizeof(TY) == 2 ? 8 : 4;
@@ -414,7 +415,7 @@ cudaError_t launch_moe_combine(const void *y, int64_t ldy, int y_dtype, const fl
                                int topk, int n, void *out, int64_t ldo, int out_dtype, int accumulate,
                                cudaStream_t st) {
   const CombineArgs a{y, ldy, w, pair_slot, out, ldo, T, topk, n, accumulate};
-  RowGrid l = RowGrid::of(T, n / 8, kThreads, 1);
+  RowGrid l = RowGrid::of(T, n / 8, kCombineThreads, 1);
   if (T >= 152 * 8) l.grid.x = 1;
   void (*k)(CombineArgs) = y_dtype == LORA_BF16
                                ? (out_dtype == LORA_BF16 ? moe_combine_kernel<__nv_bfloat16, __nv_bfloat16>

@@ -244,7 +244,6 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
   if (warp == 2) tmem_alloc2(tslot, S::kTmemCols);
   if (warp == 0 && lane == 0) prefetch_map(&maps.W);
   pdl_wait();
-  pdl_trigger();
   const int32_t *list = a.work + WorkLists::list(a.num_slots, kListAll);
   if (warp == 3) {  // row tiles before each segment: as few as kTN allows
     const int n_list = a.work[0];
@@ -267,6 +266,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
   tc_before_sync();
   cluster_sync();  // also a CTA barrier: cum, the barriers and the TMEM address are visible
   tc_after_sync();
+  pdl_trigger();  // only now: a successor that takes TMEM must not start before this CTA has its own
   const uint32_t tmem = *tslot;
   const int F = (a.N + kPairA - 1) / kPairA, n_list = a.work[0];
   const int row_bytes = S::kMx ? a.K / 2 : a.K * 2;

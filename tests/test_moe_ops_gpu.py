@@ -248,6 +248,9 @@ SHAPES = [  # P, E, K, N, div, pattern, pad
     (129, 1, 288, 128, 1, "one", 0), (1000, 4, 256, 1000, 2, "ragged", 0), (2100, 3, 320, 264, 1, "ragged", 32),
     (2048, 2, 512, 512, 8, "even", 0), (513, 1, 160, 520, 1, "one", 0), (40, 6, 64, 64, 1, "none", 0),
     (120, 5, 128, 136, 1, "bad", 0), (900, 300, 64, 72, 1, "even", 0), (1500, 1023, 32, 8, 1, "ragged", 0),
+    # tiles of 64, 128 and 256 outputs, by how many there are
+    (5, 1, 512, 4104, 1, "one", 0), (9, 2, 320, 4360, 1, "even", 32), (70, 1, 224, 4992, 2, "one", 0),
+    (200, 2, 96, 9224, 1, "even", 0), (300, 1, 64, 1160, 1, "one", 0), (600, 3, 288, 3080, 1, "ragged", 0),
 ]
 
 
