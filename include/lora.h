@@ -103,6 +103,7 @@ typedef enum { LORA_AUTO = 0, LORA_BGMV = 1, LORA_SGMV = 2, LORA_MIXED = 3 } lor
 #define LORA_MAX_TOKENS (1 << 24)
 #define LORA_MAX_EXPERTS 1024      /* lora_moe_route: experts of a layer */
 #define LORA_MAX_ROUTE_TOPK 32     /* lora_moe_route: choices of a token */
+#define LORA_MAX_EXPERT_DIM (1 << 24)  /* d_in and d_out of an expert's projection */
 #define LORA_MX_BLOCK 32           /* elements that share a scale in the 4-bit format */
 #define LORA_SGMV_MIN_ROWS 32      /* AUTO threshold: segment rows routed to SGMV */
 #define LORA_SGMV_TILE_M 128       /* rows per SGMV tile (work-list granularity) */
@@ -390,8 +391,8 @@ int lora_moe_route(const void *logits, int64_t ld_logits, int32_t dtype, int32_t
  *   x_row_div: pair p reads x row p / x_row_div (0 or 1: row p), as in
  *      lora_layer_desc; a w13 projection sets topk.
  * Constraints: 1 <= num_experts < LORA_MAX_NUM_SLOTS; d_in and d_out positive
- * multiples of 8 (d_in of LORA_MX_BLOCK for LORA_MXFP4); W and W_scale 16-byte
- * aligned.
+ * multiples of 8 (d_in of LORA_MX_BLOCK for LORA_MXFP4) up to
+ * LORA_MAX_EXPERT_DIM; W and W_scale 16-byte aligned.
  */
 typedef struct {
   int32_t dtype;
@@ -418,7 +419,8 @@ typedef struct {
  *   y:    device, [num_tokens, d_out], row stride ldy, LORA_F32 or LORA_BF16;
  *         must not overlap x
  * Errors: null pointers, ldx < d_in, ldy < d_out, a slot count that differs,
- * ld_xscale too small -> LORA_EINVAL; an fp32 table with a bf16 y ->
+ * ld_xscale too small -> LORA_EINVAL; num_experts or a dimension too large ->
+ * LORA_ERANGE; an fp32 table with a bf16 y ->
  * LORA_EUNSUPPORTED; a pointer or row stride that is not a multiple of 16
  * bytes -> LORA_EALIGN. A kernel that gave up waiting on its pipeline is
  * reported by lora_query_status(meta) as LORA_EDEVICE.

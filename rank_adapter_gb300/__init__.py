@@ -33,7 +33,8 @@ __all__ = [
     "lora_set_slot", "lora_reset_slot", "lora_prepare_meta", "lora_prepare_meta_unshared", "lora_shrink", "lora_expand", "lora_apply",
     "lora_shrink_noalloc", "lora_noalloc_scratch_bytes", "lora_embed_shrink", "embed_shrink",
     "lora_moe_pair_slots", "moe_pair_slots",
-    "LORA_MXFP4", "LORA_SCORE_SOFTMAX", "LORA_SCORE_SIGMOID", "LORA_MAX_EXPERTS", "LORA_MAX_ROUTE_TOPK", "LORA_MX_BLOCK",
+    "LORA_MXFP4", "LORA_SCORE_SOFTMAX", "LORA_SCORE_SIGMOID", "LORA_MAX_EXPERTS", "LORA_MAX_ROUTE_TOPK",
+    "LORA_MAX_EXPERT_DIM", "LORA_MX_BLOCK",
     "lora_moe_route", "lora_moe_product", "lora_mx_quantize", "lora_mx_dequantize",
     "lora_mx_tile_scales", "lora_mx_tiles_bytes", "lora_moe_act", "lora_moe_act_mx",
     "lora_moe_combine", "ExpertDesc", "ExpertWeights", "moe_route", "moe_product", "mx4_buffers", "mx4_quantize",
@@ -50,6 +51,7 @@ LORA_MXFP4 = 2                                  # experts' weights and inputs on
 LORA_SCORE_SOFTMAX, LORA_SCORE_SIGMOID = 0, 1
 LORA_MAX_EXPERTS = 1024
 LORA_MAX_ROUTE_TOPK = 32
+LORA_MAX_EXPERT_DIM = 1 << 24
 LORA_MX_BLOCK = 32
 LORA_MAX_SLICES = 4
 LORA_MAX_NUM_SLOTS = 1024

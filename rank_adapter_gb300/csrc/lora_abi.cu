@@ -441,6 +441,7 @@ int lora_moe_product(const lora_expert_desc *desc, const lora_meta *meta, const 
       desc->x_row_div < 0 || desc->W == nullptr)
     return LORA_EINVAL;
   if (desc->num_experts < 1 || desc->num_experts >= LORA_MAX_NUM_SLOTS) return LORA_ERANGE;
+  if (desc->d_in > LORA_MAX_EXPERT_DIM || desc->d_out > LORA_MAX_EXPERT_DIM) return LORA_ERANGE;
   if (!aligned16(desc->W)) return LORA_EALIGN;
   const int64_t blocks = desc->d_in / LORA_MX_BLOCK;
   if (mx) {
@@ -484,14 +485,17 @@ int lora_mx_dequantize(const uint8_t *codes, int64_t ld_codes, const uint8_t *sc
 }
 
 size_t lora_mx_tiles_bytes(int32_t num_experts, int32_t d_out, int32_t d_in) {
-  if (num_experts < 1 || num_experts >= LORA_MAX_NUM_SLOTS || d_out < 1 || d_in < 1) return 0;
+  if (num_experts < 1 || num_experts >= LORA_MAX_NUM_SLOTS || d_out < 1 || d_in < 1 || d_out > LORA_MAX_EXPERT_DIM ||
+      d_in > LORA_MAX_EXPERT_DIM)
+    return 0;
   return (size_t)num_experts * ra::mx_tiles_out(d_out) * ra::mx_tiles_in(d_in) * ra::kMxTileBytes;
 }
 
 int lora_mx_tile_scales(const uint8_t *scales, int64_t ld_scales, int32_t num_experts, int32_t d_out, int32_t d_in,
                         uint8_t *tiles, lora_stream_t stream) {
   clear_stale_error();
-  if (num_experts < 1 || num_experts >= LORA_MAX_NUM_SLOTS) return LORA_ERANGE;
+  if (num_experts < 1 || num_experts >= LORA_MAX_NUM_SLOTS || d_out > LORA_MAX_EXPERT_DIM || d_in > LORA_MAX_EXPERT_DIM)
+    return LORA_ERANGE;
   if (d_out < 8 || d_out % 8 != 0 || d_in < LORA_MX_BLOCK || d_in % LORA_MX_BLOCK != 0) return LORA_EINVAL;
   if (scales == nullptr || tiles == nullptr || ld_scales < d_in / LORA_MX_BLOCK) return LORA_EINVAL;
   if (!aligned16(scales) || !aligned16(tiles) || ld_scales % 16 != 0) return LORA_EALIGN;

@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
   uint64_t *tempty = tfull + kRing;     // every warp has what it needs of it
   uint64_t *fin = tempty + kRing;
   uint32_t *tslot = reinterpret_cast<uint32_t *>(fin + 1);
+  int32_t *lists = reinterpret_cast<int32_t *>(tslot + 1);  // segments, row tiles of them all
   int32_t *cum = reinterpret_cast<int32_t *>(sm + S::kCumOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -243,15 +244,22 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
   }
   if (warp == 2) tmem_alloc2(tslot, S::kTmemCols);
   if (warp == 0 && lane == 0) prefetch_map(&maps.W);
+  if (S::kMx && warp == 0 && lane == 1) prefetch_map(&maps.W_scale);
   pdl_wait();
   const int32_t *list = a.work + WorkLists::list(a.num_slots, kListAll);
+  // Records of the list: segment, slot, pairs, first sorted row; unused ones hold -1.
+  auto record = [&](int i) {
+    return i < a.num_slots ? *reinterpret_cast<const int4 *>(list + i * WorkLists::kRec) : make_int4(-1, 0, 0, 0);
+  };
+  int4 head = make_int4(-1, 0, 0, 0);  // warp 3: record `lane`
   if (warp == 3) {  // row tiles before each segment: as few as kTN allows
+    head = record(lane);
     const int n_list = a.work[0];
     int base = 0;
+    int4 rec = head;
     for (int i0 = 0; i0 < n_list; i0 += 32) {
       const int i = i0 + lane;
-      const int c = i < a.num_slots ? list[i * WorkLists::kRec + 2] : 0;  // unused records hold -1
-      int incl = c > 0 ? (c + S::kTN - 1) / S::kTN : 0;
+      int incl = rec.z > 0 ? (rec.z + S::kTN - 1) / S::kTN : 0;
       const int mine = incl;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -260,18 +268,23 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
       }
       if (i < n_list) cum[i] = base + incl - mine;
       base += __shfl_sync(0xffffffffu, incl, 31);
+      if (i0 + 32 < n_list) rec = record(i + 32);
     }
-    if (lane == 0) cum[n_list] = base;
+    if (lane == 0) {
+      cum[n_list] = base;
+      lists[0] = n_list;
+      lists[1] = base;
+    }
   }
   tc_before_sync();
   cluster_sync();  // also a CTA barrier: cum, the barriers and the TMEM address are visible
   tc_after_sync();
   pdl_trigger();  // only now: a successor that takes TMEM must not start before this CTA has its own
   const uint32_t tmem = *tslot;
-  const int F = (a.N + kPairA - 1) / kPairA, n_list = a.work[0];
+  const int F = (a.N + kPairA - 1) / kPairA, n_list = lists[0];
   const int row_bytes = S::kMx ? a.K / 2 : a.K * 2;
   const int nkb = (row_bytes + kStepBytes - 1) / kStepBytes;
-  const int64_t n_tiles = (int64_t)cum[n_list] * F, t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
+  const int64_t n_tiles = (int64_t)lists[1] * F, t0 = blockIdx.x >> 1, dt = gridDim.x >> 1;
   const uint32_t n_items = n_tiles > t0 ? (uint32_t)((n_tiles - t0 + dt - 1) / dt) : 0u;  // tiles of this pair
   constexpr int kElemsPerStep = S::kMx ? kStepBytes : kStepBytes / 2;  // in units of the tensor maps' elements
   // Item `item` of this pair, once it is described (nullptr: the wait ran out), and its release.
@@ -360,7 +373,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
         if ((int64_t)cum[mid] * F <= t) lo = mid;
         else hi = mid - 1;
       }
-      const int4 rec = *reinterpret_cast<const int4 *>(list + lo * WorkLists::kRec);  // segment, slot, pairs, first sorted row
+      int4 rec;
+      if (lo < 32) {
+        rec.y = __shfl_sync(0xffffffffu, head.y, lo);
+        rec.z = __shfl_sync(0xffffffffu, head.z, lo);
+        rec.w = __shfl_sync(0xffffffffu, head.w, lo);
+      } else {
+        rec = record(lo);
+      }
       const int ntt = cum[lo + 1] - cum[lo];
       const int64_t local = t - (int64_t)cum[lo] * F;
       const int f = (int)(local / ntt), tt = (int)(local - (int64_t)f * ntt);

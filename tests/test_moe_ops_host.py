@@ -20,6 +20,7 @@ def test_constants_match_the_header(ra):
     src = open(os.path.join(ROOT, "include", "lora.h")).read()
     for name in ("LORA_MAX_EXPERTS", "LORA_MAX_ROUTE_TOPK", "LORA_MX_BLOCK"):
         assert int(re.search(rf"#define {name} (\d+)", src).group(1)) == getattr(ra, name)
+    assert re.search(r"#define LORA_MAX_EXPERT_DIM \(1 << 24\)", src) and ra.LORA_MAX_EXPERT_DIM == 1 << 24
     assert re.search(rf"LORA_MXFP4 = {ra.LORA_MXFP4}\b", src)
     assert re.search(rf"LORA_SCORE_SOFTMAX = {ra.LORA_SCORE_SOFTMAX}, LORA_SCORE_SIGMOID = {ra.LORA_SCORE_SIGMOID}\b", src)
 
@@ -58,7 +59,8 @@ def test_product(ra):
                dict(y=0), dict(ldx=56), dict(ldy=24), dict(ydt=ra.LORA_MXFP4), {**mx, "ws": 0}, {**mx, "xs": 0},
                {**mx, "K": 40, "ldx": 64}, {**mx, "lxs": 0}):
         assert f(**kw) == ra.LORA_EINVAL, kw
-    for kw in (dict(E=0, S=1), dict(E=1024, S=1025), dict(T=-1)):
+    for kw in (dict(E=0, S=1), dict(E=1024, S=1025), dict(T=-1), dict(K=(1 << 24) + 8, ldx=1 << 25),
+               dict(N=(1 << 24) + 8, ldy=1 << 25)):
         assert f(**kw) == ra.LORA_ERANGE, kw
     for kw in (dict(W=P + 8), dict(x=P + 8), dict(y=P + 2), dict(ldx=68), dict(ldy=36), {**mx, "ws": P + 8},
                {**mx, "xs": P + 4}, {**mx, "lxs": 20}, {**mx, "ldx": 80}):
@@ -83,7 +85,7 @@ def test_mx(ra):
 def test_tile_scales(ra):
     def f(s=P, ld=16, E=3, N=40, K=96, t=P):
         return ra.lora_mx_tile_scales(s, ld, E, N, K, t, 0)
-    for kw in (dict(E=0), dict(E=1024)):
+    for kw in (dict(E=0), dict(E=1024), dict(N=(1 << 24) + 8), dict(K=(1 << 24) + 32, ld=1 << 20)):
         assert f(**kw) == ra.LORA_ERANGE, kw
     for kw in (dict(N=0), dict(N=12), dict(K=0), dict(K=40), dict(s=0), dict(t=0), dict(ld=0)):
         assert f(**kw) == ra.LORA_EINVAL, kw
