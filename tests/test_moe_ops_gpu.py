@@ -489,3 +489,37 @@ def test_offsets_past_32_bits(lib, dt):
         meta.prepare(torch.full((3,), E, dtype=torch.int32, device="cuda"))
         lib.moe_product(lib.ExpertWeights(Wb), meta, xb, yb)
         assert np.array_equal(f64(yb), f64(xb) @ f64(Wb[E - 1]).T)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "mx4"])
+def test_products_on_two_streams_at_once(lib, dt):
+    """Two layers' products on one metadata and two streams, many in flight, bitwise what one stream gives."""
+    P, E, K, N = 700, 5, 512, 1032
+    g = torch.Generator(device="cuda").manual_seed(11)
+    meta = lib.TokenMeta(P, E + 1)
+    meta.prepare(torch.from_numpy(slots_of("ragged", P, E, 3)).cuda())
+    sides = []
+    for _ in range(2):
+        x, W = torch.randn(P, K, device="cuda", generator=g), torch.randn(E, N, K, device="cuda", generator=g)
+        if dt == "mx4":
+            (xc, xs), (wc, ws) = lib.mx4_quantize(x), lib.mx4_quantize(W.reshape(-1, K))
+            sides.append((lib.ExpertWeights(wc.view(E, N, -1), ws.view(E, N, -1)), xc, xs))
+        else:
+            sides.append((lib.ExpertWeights(W.bfloat16()), x.bfloat16(), None))
+    want = []
+    for e, x, xs in sides:
+        y = torch.zeros(P, N, device="cuda")
+        lib.moe_product(e, meta, x, y, x_scale=xs)
+        want.append(y)
+    torch.cuda.synchronize()
+    got = [[torch.zeros(P, N, device="cuda") for _ in range(6)] for _ in sides]
+    streams = [torch.cuda.Stream() for _ in sides]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for (e, x, xs), ys, s in zip(sides, got, streams):
+            lib.moe_product(e, meta, x, ys[i], x_scale=xs, stream=s)
+    torch.cuda.synchronize()
+    assert lib.lora_query_status(meta.c) == (lib.LORA_OK, 0)
+    for ys, w in zip(got, want):
+        for y in ys:
+            assert torch.equal(y, w)
