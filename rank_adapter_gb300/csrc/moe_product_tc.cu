@@ -68,8 +68,9 @@ struct Shape {
   static constexpr int kTmemCols = kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
   static_assert(kUsedCols <= 512, "TMEM");
   static constexpr int kBarriers = 4 * STAGES_ + 2 * ACC_ + 2 * kRing + 1;
-  static constexpr int kTurnOff = STAGES_ * kStageBytes;         // the epilogue warps' 32 x 32 blocks
-  static constexpr int kRingOff = kTurnOff + 4 * 32 * 32 * 4;
+  static constexpr int kTurnOff = STAGES_ * kStageBytes;         // the epilogue warps' blocks of 32 rows
+  static constexpr int kTurnBytes = 32 * (32 + 4) * 4;
+  static constexpr int kRingOff = kTurnOff + 4 * kTurnBytes;
   static constexpr int kBarOff = kRingOff + kRing * (int)sizeof(TileInfo<TN_>);
   static constexpr int kCumOff = kBarOff + kBarriers * 8 + 16;
   static constexpr int kSmem = 1024 + kCumOff + LORA_MAX_NUM_SLOTS * 4;
@@ -171,6 +172,25 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t sdesc) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
       "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+// 16 lanes by 32 columns, without waiting: register 4 i + {0, 1} holds row
+// lane / 4, columns 8 i + 2 (lane % 4) + {0, 1}, register 4 i + {2, 3} row 8 + lane / 4.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr) : "memory");
+}
+// Two fp32 values, rounded to nearest, as bf16 (the first in the low half).
+__device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Four 8 x 8 blocks of 16-bit elements, transposed; lane l gives the address of row l % 8 of block l / 8.
+__device__ __forceinline__ void store_transposed(uint32_t addr, const uint32_t (&p)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+               ::"r"(addr), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]) : "memory");
 }
 // kind::f16: fp32 accumulator, bf16 A and B, both K-major.
 __device__ __forceinline__ uint32_t idesc_bf16_kk(int N) {
@@ -404,14 +424,15 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
       if (lane == 0) mbar_arrive(&tfull[item % kRing]);
     }
   } else if (warp < kRowWarp) {
-    // ---- accumulator -> y. A lane reads one output of 32 rows; the warp turns
-    // them round in shared memory (32 rows of 32 outputs) so that a row leaves
-    // in 16-byte pieces (stored from the lanes, two bytes each, the w2 prefill
-    // took 669 us instead of 558).
+    // ---- accumulator -> y, 32 rows of this warp's 32 outputs at a time, turned
+    // round in shared memory so that a row leaves in 16-byte pieces (stored from
+    // the lanes, two bytes each, the w2 prefill took 669 us instead of 558).
     constexpr int kVec = 16 / sizeof(TY), kPieces = 32 / kVec, kRowsAtOnce = 32 / kPieces;
+    constexpr int kPitch = 32 + kVec;  // elements a row of the block: a piece more, which spreads the banks
     const int q = warp & 3;
-    TY *y = static_cast<TY *>(a.y), *turn = reinterpret_cast<TY *>(sm + S::kTurnOff) + q * 32 * 32;
+    TY *y = static_cast<TY *>(a.y), *turn = reinterpret_cast<TY *>(sm + S::kTurnOff + q * S::kTurnBytes);
     const int piece = lane % kPieces, sub = lane / kPieces;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     for (uint32_t item = 0; item < n_items; ++item) {
       const uint32_t acc = item % S::kAcc;
       const Info *ti = tile(item);
@@ -419,19 +440,66 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
       const int f = ti->f0 + (int)rank * kRowsA + q * 32 + piece * kVec, n = ti->rows;
       if (!mbar_wait_warp(&accf[acc], (item / S::kAcc) & 1, a.err, kErrProduct)) break;
       tc_after_sync();
-      for (int c = 0; c < n; c += 32) {
-        float v[32];
-        tmem_ld32_async(tmem + ((uint32_t)(q * 32) << 16) + acc * S::kTN + c, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) turn[j * 32 + lane] = Elem<TY>::from_f(v[j]);
+      // The block in `turn` to its rows of y.
+      auto rows_out = [&](int c) {
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 32; j += kRowsAtOnce) {
-          const uint4 u = *reinterpret_cast<const uint4 *>(turn + (j + sub) * 32 + piece * kVec);
+          const uint4 u = *reinterpret_cast<const uint4 *>(turn + (j + sub) * kPitch + piece * kVec);
           if (c + j + sub < n && f < a.N) *reinterpret_cast<uint4 *>(y + (int64_t)ti->y[c + j + sub] * a.ldy + f) = u;
         }
         __syncwarp();
+      };
+      if constexpr (sizeof(TY) == 2) {
+        // Fragments of 16 outputs by 8 rows, packed to bf16 and stored transposed,
+        // four 8 x 8 blocks an instruction. (A lane an output, 32 two-byte stores: the epilogue bound
+        // products over a short d_in, 1088 in 4 bits 39.5 us, now XX us.)
+        uint32_t va[2][16];
+        auto request = [&](uint32_t(&v)[2][16], int c) {
+          tmem_ld_16x32(lanes + acc * S::kTN + c, v[0]);
+          tmem_ld_16x32(lanes + (16u << 16) + acc * S::kTN + c, v[1]);
+        };
+        const uint32_t at = smem_addr(turn) + (uint32_t)((lane >> 4) * 8 + (lane & 7)) * (kPitch * 2) + ((lane >> 3) & 1) * 16;
+        auto put = [&](uint32_t(&v)[2][16], int c) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t p[4];
+#pragma unroll
+              for (int m = 0; m < 4; ++m) p[m] = pack_bf16(v[h][8 * i + 2 * m], v[h][8 * i + 2 * m + 1]);
+              store_transposed(at + (uint32_t)(16 * i * kPitch * 2 + 32 * h), p);
+            }
+          rows_out(c);
+        };
+        if constexpr (S::kMx) {  // registers for one block only
+          for (int c = 0; c < n; c += 32) {
+            request(va, c);
+            tmem_wait_ld();
+            put(va, c);
+          }
+        } else {
+          uint32_t vb[2][16];
+          request(va, 0);
+          for (int c = 0; c < n; c += 64) {
+            tmem_wait_ld();
+            if (c + 32 < n) request(vb, c + 32);
+            put(va, c);
+            if (c + 32 >= n) break;
+            tmem_wait_ld();
+            if (c + 64 < n) request(va, c + 64);
+            put(vb, c + 32);
+          }
+        }
+      } else {
+        for (int c = 0; c < n; c += 32) {
+          float v[32];
+          tmem_ld32_async(lanes + acc * S::kTN + c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) turn[j * kPitch + lane] = v[j];
+          rows_out(c);
+        }
       }
       release(item);
       tc_before_sync();
