@@ -24,10 +24,10 @@
 // What bounds it (w2 prefill: 32744 rows of 16 experts, 2048 by 7168; w13:
 // 7168 by 4096): few rows, the weights' bytes (7.0 to 7.5 TB/s); bf16 prefill
 // the tensor pipe, 93 % active, and the power cap (w2 521 us, 1.84 PFLOP/s,
-// in short runs); 4-bit prefill shared memory, whose operand reads and writes
-// fill some three quarters of its cycles, and the scale copies in the tensor
-// pipe's order (w13 373 us, 5.2 PFLOP/s); one or two experts' few tiles the
-// pipeline's round trip, about 0.2 us a stage.
+// in short runs); 4-bit prefill no single unit (tensor pipe 53 % active, shared
+// memory 63 % busy) but the order of scale copies and MMAs in the tensor pipe
+// (w13 370 us, 5.2 PFLOP/s); one or two experts' few tiles the pipeline's round
+// trip, about 0.2 us a stage.
 #include <atomic>
 
 #include "mx.cuh"
