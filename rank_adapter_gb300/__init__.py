@@ -524,15 +524,27 @@ def _dt(t) -> int:
 
 def _rows(t, rows: int, width: int, name: str):
     """(data pointer, row stride) of a 2-D tensor of at least ``rows`` contiguous rows, ``width`` wide."""
-    shape, strides = t.shape, t.stride()
-    if len(shape) != 2 or shape[1] != width or shape[0] < rows or (strides[1] != 1 and width > 1):
-        raise ValueError(f"{name}: expected [{rows}, {width}] with contiguous rows, got shape {tuple(shape)}, "
-                         f"strides {strides}")
-    if shape[0] > 1:
-        return t.data_ptr(), strides[0]
+    have, wide = t.shape if t.dim() == 2 else (-1, -1)
+    ld, step = t.stride() if wide == width else (0, 0)
+    if wide != width or have < rows or (step != 1 and width > 1):
+        raise ValueError(f"{name}: expected [{rows}, {width}] with contiguous rows, got shape {tuple(t.shape)}, "
+                         f"strides {t.stride()}")
+    if have > 1:
+        return t.data_ptr(), ld
     # A single row's stride means nothing (torch may report any value): its length, rounded to the ABI's 16 bytes.
     es = t.element_size()
     return t.data_ptr(), -(-width * es // 16) * 16 // es
+
+
+def _mat(t, rows: int, width: int, name: str):
+    """_rows of a bf16 or fp32 tensor, and its type."""
+    try:
+        (have, wide), (ld, step), dt = t.shape, t.stride(), _dtypes[t.dtype]
+    except (KeyError, ValueError):  # another type or rank, or the first call
+        return (*_rows(t, rows, width, name), _dt(t))
+    if wide == width and have >= rows and have > 1 and step == 1:
+        return t.data_ptr(), ld, dt
+    return (*_rows(t, rows, width, name), dt)
 
 
 def _bytes(t, rows: int, width: Optional[int], name: str):
@@ -546,7 +558,7 @@ def _vec(t, n: int, name: str):
     """Data pointer of a contiguous tensor of n 32-bit elements (0 for None)."""
     if t is None:
         return 0
-    if t.numel() != n or t.element_size() != 4 or not t.is_contiguous():
+    if t.numel() != n or not t.is_contiguous() or t.element_size() != 4:
         raise ValueError(f"{name}: expected {n} contiguous 32-bit elements, got {tuple(t.shape)} {t.dtype}")
     return t.data_ptr()
 
@@ -602,7 +614,7 @@ def moe_route(logits, topk: int, score="softmax", renormalize: bool = True, scal
 
     ``pair_slot`` (int32 [T * topk]): when given, also receives the pairs' product slots."""
     T, E = logits.shape
-    lp, ld = _rows(logits, T, E, "logits")
+    lp, ld, dt = _mat(logits, T, E, "logits")
     if topk_ids is None or topk_w is None:
         import torch
         if topk_ids is None:
@@ -610,7 +622,7 @@ def moe_route(logits, topk: int, score="softmax", renormalize: bool = True, scal
         if topk_w is None:
             topk_w = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
     n = T * topk
-    check(_lib.lora_moe_route(lp, ld if ld > E else E, _dt(logits), T, E, topk, _SCORES.get(score, score), renormalize,
+    check(_lib.lora_moe_route(lp, ld if ld > E else E, dt, T, E, topk, _SCORES.get(score, score), renormalize,
                               scale, _vec(expert_map, E, "expert_map"), E if local_experts is None else local_experts,
                               _vec(topk_ids, n, "topk_ids"), _vec(topk_w, n, "topk_w"), _vec(pair_slot, n, "pair_slot"),
                               _stream(stream)), "lora_moe_route")
@@ -632,11 +644,11 @@ def moe_product(experts: ExpertWeights, meta: TokenMeta, x, y, x_scale=None, str
         sp, lds = _bytes(x_scale, rows, None, "x_scale")
         ldx *= 2
     else:
-        if _dt(x) != d.dtype:
+        xp, ldx, dt = _mat(x, rows, d_in, "x")
+        if dt != d.dtype:
             raise TypeError(f"moe_product: x of {x.dtype} does not go with the experts' weights")
-        xp, ldx = _rows(x, rows, d_in, "x")
-    yp, ldy = _rows(y, P, d.d_out, "y")
-    check(_lib.lora_moe_product(ctypes.byref(d), ctypes.byref(meta.c), xp, ldx, sp, lds, yp, ldy, _dt(y),
+    yp, ldy, ydt = _mat(y, P, d.d_out, "y")
+    check(_lib.lora_moe_product(ctypes.byref(d), ctypes.byref(meta.c), xp, ldx, sp, lds, yp, ldy, ydt,
                                 _stream(stream)), "lora_moe_product")
 
 
@@ -653,29 +665,29 @@ def mx4_quantize(x, codes=None, scales=None, stream=None):
     if codes is None or scales is None:
         c, s = mx4_buffers(rows, cols, x.device)
         codes, scales = c if codes is None else codes, s if scales is None else scales
-    xp, ldx = _rows(x, rows, cols, "x")
+    xp, ldx, dt = _mat(x, rows, cols, "x")
     cp, ldc = _bytes(codes, rows, cols // 2, "codes")
     sp, lds = _bytes(scales, rows, None, "scales")
-    check(_lib.lora_mx_quantize(xp, ldx, _dt(x), rows, cols, cp, ldc, sp, lds, _stream(stream)), "lora_mx_quantize")
+    check(_lib.lora_mx_quantize(xp, ldx, dt, rows, cols, cp, ldc, sp, lds, _stream(stream)), "lora_mx_quantize")
     return codes, scales
 
 
 def mx4_dequantize(codes, scales, y, stream=None):
     """y [rows, cols] = the values that codes and scales stand for (see lora_mx_dequantize)."""
     rows, cols = y.shape
-    yp, ldy = _rows(y, rows, cols, "y")
+    yp, ldy, dt = _mat(y, rows, cols, "y")
     cp, ldc = _bytes(codes, rows, cols // 2, "codes")
     sp, lds = _bytes(scales, rows, None, "scales")
-    check(_lib.lora_mx_dequantize(cp, ldc, sp, lds, rows, cols, yp, ldy, _dt(y), _stream(stream)), "lora_mx_dequantize")
+    check(_lib.lora_mx_dequantize(cp, ldc, sp, lds, rows, cols, yp, ldy, dt, _stream(stream)), "lora_mx_dequantize")
     return y
 
 
 def moe_act(y13, h, pair_slot=None, stream=None):
     """h[p] = silu(gate) * up of y13's rows [gate | up], for pairs with a slot (see lora_moe_act)."""
     P, inter = h.shape
-    yp, ldy = _rows(y13, P, 2 * inter, "y13")
-    hp, ldh = _rows(h, P, inter, "h")
-    check(_lib.lora_moe_act(yp, ldy, _dt(y13), _vec(pair_slot, P, "pair_slot"), P, inter, hp, ldh, _dt(h),
+    yp, ldy, ydt = _mat(y13, P, 2 * inter, "y13")
+    hp, ldh, hdt = _mat(h, P, inter, "h")
+    check(_lib.lora_moe_act(yp, ldy, ydt, _vec(pair_slot, P, "pair_slot"), P, inter, hp, ldh, hdt,
                             _stream(stream)), "lora_moe_act")
     return h
 
@@ -683,10 +695,10 @@ def moe_act(y13, h, pair_slot=None, stream=None):
 def moe_act_mx4(y13, codes, scales, pair_slot=None, stream=None):
     """moe_act into bf16, then mx4_quantize, in one pass (see lora_moe_act_mx)."""
     P, inter = y13.shape[0], y13.shape[1] // 2
-    yp, ldy = _rows(y13, P, 2 * inter, "y13")
+    yp, ldy, ydt = _mat(y13, P, 2 * inter, "y13")
     cp, ldc = _bytes(codes, P, inter // 2, "codes")
     sp, lds = _bytes(scales, P, None, "scales")
-    check(_lib.lora_moe_act_mx(yp, ldy, _dt(y13), _vec(pair_slot, P, "pair_slot"), P, inter, cp, ldc, sp, lds,
+    check(_lib.lora_moe_act_mx(yp, ldy, ydt, _vec(pair_slot, P, "pair_slot"), P, inter, cp, ldc, sp, lds,
                                _stream(stream)), "lora_moe_act_mx")
     return codes, scales
 
@@ -694,9 +706,9 @@ def moe_act_mx4(y13, codes, scales, pair_slot=None, stream=None):
 def moe_combine(y, topk_w, out, pair_slot=None, accumulate: bool = False, stream=None):
     """out[t] (+)= sum_k topk_w[t, k] * y[t * topk + k] over the pairs with a slot (see lora_moe_combine)."""
     (T, topk), n = topk_w.shape, out.shape[1]
-    yp, ldy = _rows(y, T * topk, n, "y")
-    op, ldo = _rows(out, T, n, "out")
-    check(_lib.lora_moe_combine(yp, ldy, _dt(y), _vec(topk_w, T * topk, "topk_w"),
-                                _vec(pair_slot, T * topk, "pair_slot"), T, topk, n, op, ldo, _dt(out), accumulate,
+    yp, ldy, ydt = _mat(y, T * topk, n, "y")
+    op, ldo, odt = _mat(out, T, n, "out")
+    check(_lib.lora_moe_combine(yp, ldy, ydt, _vec(topk_w, T * topk, "topk_w"),
+                                _vec(pair_slot, T * topk, "pair_slot"), T, topk, n, op, ldo, odt, accumulate,
                                 _stream(stream)), "lora_moe_combine")
     return out
