@@ -16,7 +16,8 @@ raise ``LoraError`` on a non-zero status.
 
 The mixture-of-experts layer around its LoRA: ``moe_route``, ``ExpertWeights`` and
 ``moe_product``, ``mx4_quantize`` / ``mx4_dequantize``, ``moe_act`` / ``moe_act_mx4`` and
-``moe_combine`` (``lora_moe_*`` and ``lora_mx_*`` in the header).
+``moe_combine`` (``lora_moe_*`` and ``lora_mx_*`` in the header). Their tensor forms are
+marshalled natively (``binding/moe_binding.cpp``), the C-named ones through ctypes.
 """
 from __future__ import annotations
 
@@ -509,58 +510,37 @@ def apply(table: SlotTable, meta: TokenMeta, x, y, buf=None, kind: int = LORA_AU
 
 # ----------------------------------------------------------------------------- the MoE layer around its LoRA
 
-_dtypes = {}
+_binding = None
+
+
+def _native():
+    """The native marshalling of these calls (binding/moe_binding.cpp), loaded at the first one."""
+    global _binding
+    if _binding is None:
+        import importlib.util
+        import torch  # noqa: F401  (its libraries come first)
+        path = os.path.join(_HERE, "_lib", "_moe_binding.so")
+        if not os.path.exists(path):
+            raise ImportError(f"rank_adapter_gb300: {path} is missing; build it with "
+                              "`python -c 'import __graft_entry__ as g; g.build()'`")
+        spec = importlib.util.spec_from_file_location("_moe_binding", path)
+        _binding = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_binding)
+    return _binding
+
+
+def _raw(stream):
+    """A raw stream for the native calls (None: the current one)."""
+    return None if stream is None else _stream(stream)
 
 
 def _dt(t) -> int:
-    if not _dtypes:
-        import torch
-        _dtypes.update({torch.bfloat16: LORA_BF16, torch.float32: LORA_F32})
-    d = _dtypes.get(t.dtype)
-    if d is None:
-        raise TypeError(f"expected a bf16 or fp32 tensor, got {t.dtype}")
-    return d
-
-
-def _rows(t, rows: int, width: int, name: str):
-    """(data pointer, row stride) of a 2-D tensor of at least ``rows`` contiguous rows, ``width`` wide."""
-    have, wide = t.shape if t.dim() == 2 else (-1, -1)
-    ld, step = t.stride() if wide == width else (0, 0)
-    if wide != width or have < rows or (step != 1 and width > 1):
-        raise ValueError(f"{name}: expected [{rows}, {width}] with contiguous rows, got shape {tuple(t.shape)}, "
-                         f"strides {t.stride()}")
-    if have > 1:
-        return t.data_ptr(), ld
-    # A single row's stride means nothing (torch may report any value): its length, rounded to the ABI's 16 bytes.
-    es = t.element_size()
-    return t.data_ptr(), -(-width * es // 16) * 16 // es
-
-
-def _mat(t, rows: int, width: int, name: str):
-    """_rows of a bf16 or fp32 tensor, and its type."""
-    try:
-        (have, wide), (ld, step), dt = t.shape, t.stride(), _dtypes[t.dtype]
-    except (KeyError, ValueError):  # another type or rank, or the first call
-        return (*_rows(t, rows, width, name), _dt(t))
-    if wide == width and have >= rows and have > 1 and step == 1:
-        return t.data_ptr(), ld, dt
-    return (*_rows(t, rows, width, name), dt)
-
-
-def _bytes(t, rows: int, width: Optional[int], name: str):
-    """_rows of a uint8 tensor (any width when None)."""
-    if t.element_size() != 1:
-        raise TypeError(f"{name}: expected uint8, got {t.dtype}")
-    return _rows(t, rows, t.shape[-1] if width is None else width, name)
-
-
-def _vec(t, n: int, name: str):
-    """Data pointer of a contiguous tensor of n 32-bit elements (0 for None)."""
-    if t is None:
-        return 0
-    if t.numel() != n or not t.is_contiguous() or t.element_size() != 4:
-        raise ValueError(f"{name}: expected {n} contiguous 32-bit elements, got {tuple(t.shape)} {t.dtype}")
-    return t.data_ptr()
+    import torch
+    if t.dtype == torch.bfloat16:
+        return LORA_BF16
+    if t.dtype == torch.float32:
+        return LORA_F32
+    raise TypeError(f"expected a bf16 or fp32 tensor, got {t.dtype}")
 
 
 class ExpertWeights:
@@ -592,6 +572,7 @@ class ExpertWeights:
             d.dtype = _dt(w)
         d.W, d.x_row_div = w.data_ptr(), x_row_div
         self.w, self.scale, self.desc = w, scale, d
+        self.address = ctypes.addressof(d)
 
     @property
     def d_in(self) -> int:
@@ -613,19 +594,17 @@ def moe_route(logits, topk: int, score="softmax", renormalize: bool = True, scal
     """(topk_ids int32 [T, topk], topk_w fp32 [T, topk]) for logits [T, E] (see lora_moe_route).
 
     ``pair_slot`` (int32 [T * topk]): when given, also receives the pairs' product slots."""
-    T, E = logits.shape
-    lp, ld, dt = _mat(logits, T, E, "logits")
     if topk_ids is None or topk_w is None:
         import torch
+        shape = (logits.shape[0], topk)
         if topk_ids is None:
-            topk_ids = torch.empty(T, topk, dtype=torch.int32, device=logits.device)
+            topk_ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
         if topk_w is None:
-            topk_w = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
-    n = T * topk
-    check(_lib.lora_moe_route(lp, ld if ld > E else E, dt, T, E, topk, _SCORES.get(score, score), renormalize,
-                              scale, _vec(expert_map, E, "expert_map"), E if local_experts is None else local_experts,
-                              _vec(topk_ids, n, "topk_ids"), _vec(topk_w, n, "topk_w"), _vec(pair_slot, n, "pair_slot"),
-                              _stream(stream)), "lora_moe_route")
+            topk_w = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    st = (_binding or _native()).moe_route(logits, topk, _SCORES.get(score, score), renormalize, scale, expert_map,
+                                           local_experts, topk_ids, topk_w, pair_slot, _raw(stream))
+    if st:
+        check(st, "lora_moe_route")
     return topk_ids, topk_w
 
 
@@ -634,22 +613,9 @@ def moe_product(experts: ExpertWeights, meta: TokenMeta, x, y, x_scale=None, str
 
     ``meta``: prepared over the pairs' product slots. x: [rows, d_in] of the weights' type; with 4-bit weights
     the codes [rows, d_in / 2] and ``x_scale`` [rows, ld] of mx4_quantize."""
-    d, P = experts.desc, meta.c.num_tokens
-    rows, d_in = -(-P // max(1, d.x_row_div)), d.d_in
-    sp = lds = 0
-    if d.dtype == LORA_MXFP4:
-        if x_scale is None:
-            raise TypeError("moe_product: 4-bit weights take x as mx4_quantize gives it, with x_scale")
-        xp, ldx = _bytes(x, rows, d_in // 2, "x")
-        sp, lds = _bytes(x_scale, rows, None, "x_scale")
-        ldx *= 2
-    else:
-        xp, ldx, dt = _mat(x, rows, d_in, "x")
-        if dt != d.dtype:
-            raise TypeError(f"moe_product: x of {x.dtype} does not go with the experts' weights")
-    yp, ldy, ydt = _mat(y, P, d.d_out, "y")
-    check(_lib.lora_moe_product(ctypes.byref(d), ctypes.byref(meta.c), xp, ldx, sp, lds, yp, ldy, ydt,
-                                _stream(stream)), "lora_moe_product")
+    st = (_binding or _native()).moe_product(experts.address, ctypes.addressof(meta.c), x, y, x_scale, _raw(stream))
+    if st:
+        check(st, "lora_moe_product")
 
 
 def mx4_buffers(rows: int, cols: int, device="cuda"):
@@ -661,54 +627,42 @@ def mx4_buffers(rows: int, cols: int, device="cuda"):
 
 def mx4_quantize(x, codes=None, scales=None, stream=None):
     """(codes, scales) of the rows of x [rows, cols] in the microscaled 4-bit format (see lora_mx_quantize)."""
-    rows, cols = x.shape
     if codes is None or scales is None:
-        c, s = mx4_buffers(rows, cols, x.device)
+        c, s = mx4_buffers(x.shape[0], x.shape[1], x.device)
         codes, scales = c if codes is None else codes, s if scales is None else scales
-    xp, ldx, dt = _mat(x, rows, cols, "x")
-    cp, ldc = _bytes(codes, rows, cols // 2, "codes")
-    sp, lds = _bytes(scales, rows, None, "scales")
-    check(_lib.lora_mx_quantize(xp, ldx, dt, rows, cols, cp, ldc, sp, lds, _stream(stream)), "lora_mx_quantize")
+    st = (_binding or _native()).mx4_quantize(x, codes, scales, _raw(stream))
+    if st:
+        check(st, "lora_mx_quantize")
     return codes, scales
 
 
 def mx4_dequantize(codes, scales, y, stream=None):
     """y [rows, cols] = the values that codes and scales stand for (see lora_mx_dequantize)."""
-    rows, cols = y.shape
-    yp, ldy, dt = _mat(y, rows, cols, "y")
-    cp, ldc = _bytes(codes, rows, cols // 2, "codes")
-    sp, lds = _bytes(scales, rows, None, "scales")
-    check(_lib.lora_mx_dequantize(cp, ldc, sp, lds, rows, cols, yp, ldy, dt, _stream(stream)), "lora_mx_dequantize")
+    st = (_binding or _native()).mx4_dequantize(y, codes, scales, _raw(stream))
+    if st:
+        check(st, "lora_mx_dequantize")
     return y
 
 
 def moe_act(y13, h, pair_slot=None, stream=None):
     """h[p] = silu(gate) * up of y13's rows [gate | up], for pairs with a slot (see lora_moe_act)."""
-    P, inter = h.shape
-    yp, ldy, ydt = _mat(y13, P, 2 * inter, "y13")
-    hp, ldh, hdt = _mat(h, P, inter, "h")
-    check(_lib.lora_moe_act(yp, ldy, ydt, _vec(pair_slot, P, "pair_slot"), P, inter, hp, ldh, hdt,
-                            _stream(stream)), "lora_moe_act")
+    st = (_binding or _native()).moe_act(y13, h, pair_slot, _raw(stream))
+    if st:
+        check(st, "lora_moe_act")
     return h
 
 
 def moe_act_mx4(y13, codes, scales, pair_slot=None, stream=None):
     """moe_act into bf16, then mx4_quantize, in one pass (see lora_moe_act_mx)."""
-    P, inter = y13.shape[0], y13.shape[1] // 2
-    yp, ldy, ydt = _mat(y13, P, 2 * inter, "y13")
-    cp, ldc = _bytes(codes, P, inter // 2, "codes")
-    sp, lds = _bytes(scales, P, None, "scales")
-    check(_lib.lora_moe_act_mx(yp, ldy, ydt, _vec(pair_slot, P, "pair_slot"), P, inter, cp, ldc, sp, lds,
-                               _stream(stream)), "lora_moe_act_mx")
+    st = (_binding or _native()).moe_act_mx4(y13, codes, scales, pair_slot, _raw(stream))
+    if st:
+        check(st, "lora_moe_act_mx")
     return codes, scales
 
 
 def moe_combine(y, topk_w, out, pair_slot=None, accumulate: bool = False, stream=None):
     """out[t] (+)= sum_k topk_w[t, k] * y[t * topk + k] over the pairs with a slot (see lora_moe_combine)."""
-    (T, topk), n = topk_w.shape, out.shape[1]
-    yp, ldy, ydt = _mat(y, T * topk, n, "y")
-    op, ldo, odt = _mat(out, T, n, "out")
-    check(_lib.lora_moe_combine(yp, ldy, ydt, _vec(topk_w, T * topk, "topk_w"),
-                                _vec(pair_slot, T * topk, "pair_slot"), T, topk, n, op, ldo, odt, accumulate,
-                                _stream(stream)), "lora_moe_combine")
+    st = (_binding or _native()).moe_combine(y, topk_w, out, pair_slot, accumulate, _raw(stream))
+    if st:
+        check(st, "lora_moe_combine")
     return out
