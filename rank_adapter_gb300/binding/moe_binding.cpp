@@ -10,6 +10,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <string>
+#include <type_traits>
 
 #include "lora.h"
 
@@ -47,7 +48,7 @@ struct Mat {
                                           "] with contiguous rows, got " + describe(t)};
     const at::ScalarType st = t.scalar_type();
     dtype = st == at::kBFloat16 ? LORA_BF16 : LORA_F32;
-    if (bytes ? t.element_size() != 1 : st != at::kBFloat16 && st != at::kFloat)
+    if (bytes ? st != at::kByte : st != at::kBFloat16 && st != at::kFloat)
       throw Refused{PyExc_TypeError, std::string(name) + ": expected " + (bytes ? "uint8" : "bf16 or fp32") + ", got " +
                                          c10::toString(st)};
     // A single row's stride means nothing (torch may report any value): its length, rounded to the ABI's 16 bytes.
@@ -57,13 +58,14 @@ struct Mat {
   }
 };
 
-// n contiguous 32-bit elements; None gives a null pointer.
+// n contiguous int32 or fp32 elements; None gives a null pointer.
 template <typename T> T *vec(PyObject *o, int64_t n, const char *name) {
   if (o == Py_None) return nullptr;
   const at::Tensor &t = tensor(o, name);
-  if (t.numel() != n || !t.is_contiguous() || t.element_size() != 4)
-    throw Refused{PyExc_ValueError, std::string(name) + ": expected " + std::to_string(n) +
-                                        " contiguous 32-bit elements, got " + describe(t) + " " +
+  constexpr at::ScalarType want = std::is_floating_point_v<T> ? at::kFloat : at::kInt;
+  if (t.numel() != n || !t.is_contiguous() || t.scalar_type() != want)
+    throw Refused{PyExc_ValueError, std::string(name) + ": expected " + std::to_string(n) + " contiguous " +
+                                        c10::toString(want) + " elements, got " + describe(t) + " " +
                                         c10::toString(t.scalar_type())};
   return static_cast<T *>(t.data_ptr());
 }

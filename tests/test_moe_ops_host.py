@@ -146,3 +146,41 @@ def test_binding_checks_shapes(ra):
         ra.mx4_dequantize(z(3, 16, dtype=torch.uint8), z(3, 16, dtype=torch.uint8), z(4, 32))
     with pytest.raises(ValueError):
         ra.moe_route(z(4, 32).t(), 2)
+    for bad in (lambda: ra.moe_act(z(4, 32), z(4, 16), pair_slot=z(4)),                                   # slots not int32
+                lambda: ra.moe_act(z(4, 32), z(4, 16), pair_slot=z(3, dtype=torch.int32)),
+                lambda: ra.moe_combine(z(4, 16), z(2, 2, dtype=torch.int32), z(2, 16)),                   # weights not fp32
+                lambda: ra.moe_route(z(4, 8), 2, expert_map=z(7, dtype=torch.int32), topk_ids=z(4, 2, dtype=torch.int32),
+                                     topk_w=z(4, 2)),
+                lambda: ra.mx4_quantize(z(64, 2).t())):
+        with pytest.raises(ValueError):
+            bad()
+    u8 = dict(dtype=torch.uint8)
+    for bad in (lambda: ra.moe_act(z(4, 32, dtype=torch.float16), z(4, 16)), lambda: ra.moe_act([1], z(4, 16)),
+                lambda: ra.mx4_quantize(z(3, 32), z(3, 16), z(3, 16, **u8)),
+                lambda: ra.mx4_dequantize(z(3, 16, **u8), z(3, 16, **u8), z(3, 32, dtype=torch.int32)),
+                lambda: ra.moe_route(z(4, 8), "two", topk_ids=z(4, 2, dtype=torch.int32), topk_w=z(4, 2))):
+        with pytest.raises(TypeError):
+            bad()
+
+
+def test_product_binding_checks(ra):
+    import torch
+    z, u8 = torch.zeros, dict(dtype=torch.uint8)
+
+    class Meta:                                         # what moe_product reads of a TokenMeta
+        c = ra.Meta()
+    Meta.c.num_tokens = 6
+    w = ra.ExpertWeights(z(2, 16, 32), x_row_div=3)
+    for x, y in ((z(1, 32), z(6, 16)), (z(2, 24), z(6, 16)), (z(2, 32), z(5, 16)), (z(2, 32), z(6, 24))):
+        with pytest.raises(ValueError):
+            ra.moe_product(w, Meta, x, y)
+    for x in (z(2, 32).bfloat16(), z(2, 32, **u8), None):
+        with pytest.raises(TypeError):
+            ra.moe_product(w, Meta, x, z(6, 16))
+    w.desc.dtype = ra.LORA_MXFP4                        # as 4-bit weights: codes and scales
+    with pytest.raises(TypeError):
+        ra.moe_product(w, Meta, z(2, 16, **u8), z(6, 16))
+    with pytest.raises(TypeError):
+        ra.moe_product(w, Meta, z(2, 16), z(6, 16), x_scale=z(2, 16, **u8))
+    with pytest.raises(ValueError):
+        ra.moe_product(w, Meta, z(2, 16, **u8), z(6, 16), x_scale=z(1, 16, **u8))
