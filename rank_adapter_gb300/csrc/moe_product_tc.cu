@@ -120,6 +120,8 @@ __device__ __forceinline__ void tma_w(uint32_t dst, const CUtensorMap *map, int 
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+// Waits for all of the thread's cp.async (they are in no commit group).
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void tma_scales(uint32_t dst, const CUtensorMap *map, int c1, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
     bool ok = true;
     for (uint32_t item = 0; item < n_items && ok; ++item) {
       const Info *ti = tile(item);
-      if (ti == nullptr) break;
+      if (ti == nullptr) { ok = false; break; }
       const int f = ti->f0 + (int)rank * kRowsA, e = ti->expert;
       // The first pair of the CTA's scale tiles; outputs past the last tile take that one's (they are not stored).
       const int sf = S::kMx ? (e * mx_tiles_out(a.N) + min(f / kMxTile, mx_tiles_out(a.N) - 1)) * (mx_tiles_in(a.K) / 2) : 0;
@@ -346,6 +348,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
         __syncwarp();
       }
     }
+    // Every stage's last use, as if to fill it again: its loads have landed and
+    // its arrivals on this CTA's barriers are in. (A wait that ran out, here or
+    // above, has left the loads issued before it its whole limit to land.)
+    for (int i = 0; i < S::kStages && ok; ++i, st.next()) ok = mbar_wait_warp(&empty[st.s], st.phase ^ 1, a.err, kErrProduct);
   } else if (warp == 1) {
     // ---- passes this CTA's rows on to the leader. The rows were written by
     // ordinary stores and cp.async; the fence orders them before the tensor
@@ -515,6 +521,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(leader_addr(&acce[acc]));
     }
+    mbar_wait_warp(fin, 0, a.err, kErrProduct);  // the leader's last arrival on this CTA, right behind its last accumulator
   } else if (warp < kScaleWarp) {
     // ---- x rows: this CTA's half of the tile's rows. Two groups of four warps
     // take the stages in turn (a group needs about 640 clocks for 128 rows, an
@@ -545,7 +552,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
         cp_async_arrive(&rows[st.s]);
       }
     }
-    cp_async_wait_upto(0);
+    cp_async_wait_all();
   } else if (S::kMx && warp == kScaleWarp + S::kScaleWarps) {
     // ---- scales of a stage to TMEM (leader). A warp of its own: with these
     // copies in the MMA warp's stream its issue bound the kernel (w13 prefill
@@ -625,7 +632,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) moe_product_tc_kernel(const __
     }
   }
   tc_before_sync();
-  cluster_sync();  // no barrier of this CTA is signalled after its peer is past here
+  // No barrier of this CTA is signalled after this: the tensor core's arrivals
+  // (empty, accf, fin; both CTAs' barriers) and the loads' have been waited for
+  // in the CTA they go to, the threads' own ones come before their cluster barrier.
+  cluster_sync();
   if (warp == 2) {
     tc_after_sync();
     tmem_free2(tmem, S::kTmemCols);
