@@ -51,6 +51,8 @@ struct Mat {
     if (bytes ? st != at::kByte : st != at::kBFloat16 && st != at::kFloat)
       throw Refused{PyExc_TypeError, std::string(name) + ": expected " + (bytes ? "uint8" : "bf16 or fp32") + ", got " +
                                          c10::toString(st)};
+    if (t.size(0) > 1 && t.stride(0) < t.size(1))
+      throw Refused{PyExc_ValueError, std::string(name) + ": expected rows that do not overlap, got " + describe(t)};
     // A single row's stride means nothing (torch may report any value): its length, rounded to the ABI's 16 bytes.
     const int64_t es = (int64_t)t.element_size();
     ld = t.size(0) > 1 ? t.stride(0) : (t.size(1) * es + 15) / 16 * 16 / es;
@@ -128,7 +130,7 @@ int moe_route(PyObject *const *a) {
   lora_stream_t s = stream(a[10]);
   const int32_t t32 = narrow(T, "tokens"), e32 = narrow(E, "experts");
   return unlocked([&] {
-    return lora_moe_route(l.p, l.ld > E ? l.ld : E, l.dtype, t32, e32, topk, score, renorm, scale, map, local, ids, w,
+    return lora_moe_route(l.p, l.ld, l.dtype, t32, e32, topk, score, renorm, scale, map, local, ids, w,
                           slot, s);
   });
 }
