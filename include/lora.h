@@ -415,7 +415,8 @@ typedef struct {
  *         desc->num_experts + 1, its num_tokens the number of pairs
  *   x:    device, [ceil(num_tokens / x_row_div), d_in], row stride ldx
  *         elements, of desc->dtype (LORA_MXFP4: rows of codes, ldx / 2 bytes
- *         apart, with x_scale rows of ld_xscale bytes)
+ *         apart, with x_scale rows of ld_xscale bytes, which are read 16 at a
+ *         time: the last row's memory too reaches to a multiple of 16)
  *   y:    device, [num_tokens, d_out], row stride ldy, LORA_F32 or LORA_BF16;
  *         must not overlap x
  * Errors: null pointers, ldx < d_in, ldy < d_out, a slot count that differs,

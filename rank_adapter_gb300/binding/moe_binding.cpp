@@ -60,6 +60,22 @@ struct Mat {
   }
 };
 
+// Scale bytes of at least `rows` rows of `cols` elements: a byte a block in every row. A kernel that `loads` them
+// takes 16 at a time, so the bytes up to the next multiple of 16 belong to the tensor's memory, after the last row too.
+struct Scales : Mat {
+  Scales(PyObject *o, int64_t rows, int64_t cols, const char *name, bool loads = false) : Mat(o, rows, -1, name, true) {
+    const at::Tensor &t = tensor(o, name);
+    const int64_t blocks = cols / LORA_MX_BLOCK, row = loads ? (blocks + 15) / 16 * 16 : blocks;
+    if (t.size(1) < blocks)
+      throw Refused{PyExc_ValueError, std::string(name) + ": expected at least " + std::to_string(blocks) +
+                                          " columns, a byte for " + std::to_string(LORA_MX_BLOCK) + " elements, got " + describe(t)};
+    if (loads && rows > 0 &&
+        t.storage_offset() + (rows - 1) * ld + row > (int64_t)t.storage().nbytes())
+      throw Refused{PyExc_ValueError, std::string(name) + ": expected rows of " + std::to_string(row) +
+                                          " bytes of memory (mx4_buffers allocates them), got " + describe(t)};
+  }
+};
+
 // n contiguous int32 or fp32 elements; None gives a null pointer.
 template <typename T> T *vec(PyObject *o, int64_t n, const char *name) {
   if (o == Py_None) return nullptr;
@@ -148,7 +164,7 @@ int moe_product(PyObject *const *a) {
   const uint8_t *sp = nullptr;
   int64_t lds = 0;
   if (mx) {
-    const Mat sc(a[4], rows, -1, "x_scale", true);
+    const Scales sc(a[4], rows, d->d_in, "x_scale", true);
     sp = static_cast<const uint8_t *>(sc.p);
     lds = sc.ld;
   }
@@ -160,7 +176,8 @@ int moe_product(PyObject *const *a) {
 // (x, codes, scales, stream), (y, codes, scales, stream): rows of x or y to the 4-bit format, or from it
 template <bool kTo> int mx4(PyObject *const *a) {
   const int64_t rows = rows_of(a[0], kTo ? "x" : "y"), cols = rows_of(a[0], kTo ? "x" : "y", 1);
-  const Mat m(a[0], rows, cols, kTo ? "x" : "y"), c(a[1], rows, cols / 2, "codes", true), sc(a[2], rows, -1, "scales", true);
+  const Mat m(a[0], rows, cols, kTo ? "x" : "y"), c(a[1], rows, cols / 2, "codes", true);
+  const Scales sc(a[2], rows, cols, "scales");
   lora_stream_t s = stream(a[3]);
   const int32_t n = narrow(cols, "columns");
   uint8_t *cp = static_cast<uint8_t *>(c.p), *sp = static_cast<uint8_t *>(sc.p);
@@ -183,7 +200,8 @@ int moe_act(PyObject *const *a) {
 // (y13, codes, scales, pair_slot or None, stream)
 int moe_act_mx4(PyObject *const *a) {
   const int64_t P = rows_of(a[0], "y13"), inter = rows_of(a[0], "y13", 1) / 2;
-  const Mat y(a[0], P, 2 * inter, "y13"), c(a[1], P, inter / 2, "codes", true), sc(a[2], P, -1, "scales", true);
+  const Mat y(a[0], P, 2 * inter, "y13"), c(a[1], P, inter / 2, "codes", true);
+  const Scales sc(a[2], P, inter, "scales");
   const int32_t *slot = vec<int32_t>(a[3], P, "pair_slot");
   lora_stream_t s = stream(a[4]);
   const int32_t p32 = narrow(P, "pairs"), i32 = narrow(inter, "columns");

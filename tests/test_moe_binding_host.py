@@ -39,3 +39,29 @@ def test_every_matrix_refuses_overlapping_rows(ra):
                  lambda: ra.moe_product(ra.ExpertWeights(z(2, 16, 32)), Meta(ra, 4), z(1, 32).expand(4, 32), z(4, 16))):
         with pytest.raises(ValueError, match="overlap"):
             call()
+
+
+# One row of 512 elements has 16 scale bytes; a row of 7168 has 224.
+@pytest.mark.parametrize("rows,cols,scales", [(1, 512, z(1, 1, **U8)), (1, 512, z(1, 15, **U8)), (3, 512, z(3, 16, **U8)[:, :1]),
+                                              (5, 7168, z(5, 224, **U8)[:, :223]), (1, 7168, z(1, 209, **U8)), (2, 64, z(2, 16, **U8)[:, :1])])
+def test_narrow_scales_are_refused(ra, rows, cols, scales):
+    codes = z(rows, cols // 2, **U8)
+    for call in (lambda: ra.mx4_quantize(z(rows, cols), codes, scales),
+                 lambda: ra.mx4_dequantize(codes, scales, z(rows, cols)),
+                 lambda: ra.moe_act_mx4(z(rows, 2 * cols), codes, scales)):
+        with pytest.raises(ValueError, match="scales: expected at least"):
+            call()
+    w = ra.ExpertWeights(z(2, 16, cols // 2))
+    w.desc.dtype, w.desc.d_in = ra.LORA_MXFP4, cols
+    with pytest.raises(ValueError, match="x_scale: expected at least"):
+        ra.moe_product(w, Meta(ra, rows), codes, z(rows, 16), x_scale=scales)
+
+
+def test_x_scale_rows_are_whole_in_memory(ra):
+    """A product loads scale bytes 16 at a time: the last row's memory reaches to a multiple of 16."""
+    w = ra.ExpertWeights(z(2, 16, 96 // 2))
+    w.desc.dtype, w.desc.d_in = ra.LORA_MXFP4, 96
+    short = (z(1, 3, **U8), z(16 + 3, **U8).as_strided((2, 3), (16, 1)), z(2, 16, **U8)[1:, 3:])
+    for s in short:
+        with pytest.raises(ValueError, match="x_scale: expected rows of 16 bytes"):
+            ra.moe_product(w, Meta(ra, s.size(0)), z(s.size(0), 48, **U8), z(s.size(0), 16), x_scale=s)
