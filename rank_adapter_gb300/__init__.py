@@ -17,7 +17,8 @@ raise ``LoraError`` on a non-zero status.
 The mixture-of-experts layer around its LoRA: ``moe_route``, ``ExpertWeights`` and
 ``moe_product``, ``mx4_quantize`` / ``mx4_dequantize``, ``moe_act`` / ``moe_act_mx4`` and
 ``moe_combine`` (``lora_moe_*`` and ``lora_mx_*`` in the header). Their tensor forms are
-marshalled natively (``binding/moe_binding.cpp``), the C-named ones through ctypes.
+marshalled natively (``binding/moe_binding.cpp``), which raises for tensors of the wrong
+shape or type or not on the current CUDA device; the C-named ones go through ctypes.
 """
 from __future__ import annotations
 
@@ -563,6 +564,9 @@ class ExpertWeights:
                     or scale.shape[:2] != w.shape[:2]:
                 raise ValueError("ExpertWeights: 4-bit weights are uint8 codes [experts, d_out, d_in / 2] and contiguous "
                                  "uint8 scales [experts, d_out, ld]")
+            if not w.is_cuda or scale.device != w.device or w.device.index != torch.cuda.current_device():
+                raise ValueError(f"ExpertWeights: 4-bit weights and their scales are on the current CUDA device, got {w.device} "
+                                 f"and {scale.device}")
             d.dtype, d.d_in = LORA_MXFP4, 2 * w.shape[2]
             tiles = torch.empty(lora_mx_tiles_bytes(d.num_experts, d.d_out, d.d_in), dtype=torch.uint8, device=w.device)
             check(lora_mx_tile_scales(scale.data_ptr(), scale.shape[2], d.num_experts, d.d_out, d.d_in,
@@ -613,7 +617,8 @@ def moe_product(experts: ExpertWeights, meta: TokenMeta, x, y, x_scale=None, str
 
     ``meta``: prepared over the pairs' product slots. x: [rows, d_in] of the weights' type; with 4-bit weights
     the codes [rows, d_in / 2] and ``x_scale`` [rows, ld] of mx4_quantize."""
-    st = (_binding or _native()).moe_product(experts.address, ctypes.addressof(meta.c), x, y, x_scale, _raw(stream))
+    st = (_binding or _native()).moe_product(experts.address, ctypes.addressof(meta.c), x, y, x_scale, _raw(stream),
+                                             experts.w, getattr(meta, "token_slot", None))
     if st:
         check(st, "lora_moe_product")
 

@@ -3,9 +3,11 @@
 // (include/lora.h) on the given or the current stream. The same through ctypes
 // takes about 4.7 us a call on the host, more than most of these kernels run
 // for a decode step; this takes 2.3 us. Each function returns the lora_status;
-// arguments that are no tensors, or of the wrong shape or type, raise.
+// arguments that are no tensors, of the wrong shape or type, or not on the
+// current device raise.
 #include <Python.h>
 
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -35,13 +37,30 @@ std::string describe(const at::Tensor &t) {
   return s + ")";
 }
 
+// The tensors of a call, checked together once their shapes and types are known to be right: a kernel of the current
+// device uses them.
+class Call {
+ public:
+  void uses(const at::Tensor &t, const char *name) {
+    if (n_ < kMost && t.numel() > 0) used_[n_++] = {&t, name};
+  }
+  // The stream to launch on: a raw one, or for None the current device's current one.
+  lora_stream_t stream(PyObject *o);
+
+ private:
+  static constexpr int kMost = 8;
+  struct { const at::Tensor *t; const char *name; } used_[kMost];
+  int n_ = 0;
+};
+
 // A matrix of at least `rows` contiguous rows, `width` wide (any width when negative).
 struct Mat {
   void *p;
   int64_t ld;  // row stride in elements
   int32_t dtype;
-  Mat(PyObject *o, int64_t rows, int64_t width, const char *name, bool bytes = false) {
+  Mat(Call &call, PyObject *o, int64_t rows, int64_t width, const char *name, bool bytes = false) {
     const at::Tensor &t = tensor(o, name);
+    call.uses(t, name);
     if (t.dim() != 2 || (width >= 0 && t.size(1) != width) || t.size(0) < rows || (t.stride(1) != 1 && t.size(1) > 1))
       throw Refused{PyExc_ValueError, std::string(name) + ": expected [" + std::to_string(rows) + ", " +
                                           (width >= 0 ? std::to_string(width) : std::string("any")) +
@@ -63,7 +82,8 @@ struct Mat {
 // Scale bytes of at least `rows` rows of `cols` elements: a byte a block in every row. A kernel that `loads` them
 // takes 16 at a time, so the bytes up to the next multiple of 16 belong to the tensor's memory, after the last row too.
 struct Scales : Mat {
-  Scales(PyObject *o, int64_t rows, int64_t cols, const char *name, bool loads = false) : Mat(o, rows, -1, name, true) {
+  Scales(Call &call, PyObject *o, int64_t rows, int64_t cols, const char *name, bool loads = false)
+      : Mat(call, o, rows, -1, name, true) {
     const at::Tensor &t = tensor(o, name);
     const int64_t blocks = cols / LORA_MX_BLOCK, row = loads ? (blocks + 15) / 16 * 16 : blocks;
     if (t.size(1) < blocks)
@@ -77,9 +97,10 @@ struct Scales : Mat {
 };
 
 // n contiguous int32 or fp32 elements; None gives a null pointer.
-template <typename T> T *vec(PyObject *o, int64_t n, const char *name) {
+template <typename T> T *vec(Call &call, PyObject *o, int64_t n, const char *name) {
   if (o == Py_None) return nullptr;
   const at::Tensor &t = tensor(o, name);
+  call.uses(t, name);
   constexpr at::ScalarType want = std::is_floating_point_v<T> ? at::kFloat : at::kInt;
   if (t.numel() != n || !t.is_contiguous() || t.scalar_type() != want)
     throw Refused{PyExc_ValueError, std::string(name) + ": expected " + std::to_string(n) + " contiguous " +
@@ -108,10 +129,25 @@ bool truth(PyObject *o) {
   if (v < 0) throw Refused{nullptr, ""};
   return v != 0;
 }
-// A raw stream, or None for the current one of the current device.
-lora_stream_t stream(PyObject *o) {
-  if (o == Py_None) return (lora_stream_t)c10::cuda::getCurrentCUDAStream().stream();
-  return (lora_stream_t)(intptr_t)integer(o);
+lora_stream_t Call::stream(PyObject *o) {
+  for (int i = 0; i < n_; ++i)
+    if (!used_[i].t->is_cuda())
+      throw Refused{PyExc_ValueError, std::string(used_[i].name) + ": expected a CUDA tensor, got one on " + used_[i].t->device().str()};
+  lora_stream_t s;
+  int current;
+  if (o == Py_None) {
+    const c10::cuda::CUDAStream c = c10::cuda::getCurrentCUDAStream();
+    s = (lora_stream_t)c.stream();
+    current = (int)c.device_index();
+  } else {
+    s = (lora_stream_t)(intptr_t)integer(o);
+    current = (int)c10::cuda::current_device();
+  }
+  for (int i = 0; i < n_; ++i)
+    if ((int)used_[i].t->get_device() != current)
+      throw Refused{PyExc_ValueError, std::string(used_[i].name) + ": on " + used_[i].t->device().str() +
+                                          ", but the current device is cuda:" + std::to_string(current)};
+  return s;
 }
 int64_t rows_of(PyObject *o, const char *name, int dim = 0) {
   const at::Tensor &t = tensor(o, name);
@@ -132,18 +168,19 @@ template <typename F> int unlocked(F f) {
 
 // (logits, topk, score, renormalize, scale, expert_map, local_experts or None, topk_ids, topk_w, pair_slot, stream)
 int moe_route(PyObject *const *a) {
+  Call call;
   const int64_t T = rows_of(a[0], "logits"), E = rows_of(a[0], "logits", 1);
-  const Mat l(a[0], T, E, "logits");
+  const Mat l(call, a[0], T, E, "logits");
   const int32_t topk = int32(a[1], "topk"), score = int32(a[2], "score");
   const bool renorm = truth(a[3]);
   const float scale = (float)number(a[4]);
-  const int32_t *map = vec<int32_t>(a[5], E, "expert_map");
+  const int32_t *map = vec<int32_t>(call, a[5], E, "expert_map");
   const int32_t local = a[6] == Py_None ? narrow(E, "experts") : int32(a[6], "local_experts");
   const int64_t n = T * topk;
-  int32_t *ids = vec<int32_t>(a[7], n, "topk_ids");
-  float *w = vec<float>(a[8], n, "topk_w");
-  int32_t *slot = vec<int32_t>(a[9], n, "pair_slot");
-  lora_stream_t s = stream(a[10]);
+  int32_t *ids = vec<int32_t>(call, a[7], n, "topk_ids");
+  float *w = vec<float>(call, a[8], n, "topk_w");
+  int32_t *slot = vec<int32_t>(call, a[9], n, "pair_slot");
+  lora_stream_t s = call.stream(a[10]);
   const int32_t t32 = narrow(T, "tokens"), e32 = narrow(E, "experts");
   return unlocked([&] {
     return lora_moe_route(l.p, l.ld, l.dtype, t32, e32, topk, score, renorm, scale, map, local, ids, w,
@@ -151,34 +188,39 @@ int moe_route(PyObject *const *a) {
   });
 }
 
-// (address of the lora_expert_desc, of the lora_meta, x, y, x_scale or None, stream)
+// (address of the lora_expert_desc, of the lora_meta, x, y, x_scale or None, stream, the weights, one of the metadata's
+// tensors or None)
 int moe_product(PyObject *const *a) {
+  Call call;
   const lora_expert_desc *d = (const lora_expert_desc *)(intptr_t)integer(a[0]);
   const lora_meta *m = (const lora_meta *)(intptr_t)integer(a[1]);
   const int64_t P = m->num_tokens, div = d->x_row_div > 1 ? d->x_row_div : 1, rows = (P + div - 1) / div;
   const bool mx = d->dtype == LORA_MXFP4;
   if (mx && a[4] == Py_None)
     throw Refused{PyExc_TypeError, "moe_product: 4-bit weights take x as mx4_quantize gives it, with x_scale"};
-  const Mat x(a[2], rows, mx ? d->d_in / 2 : d->d_in, "x", mx);
+  const Mat x(call, a[2], rows, mx ? d->d_in / 2 : d->d_in, "x", mx);
   if (!mx && x.dtype != d->dtype) throw Refused{PyExc_TypeError, "moe_product: x is not of the experts' weights' type"};
   const uint8_t *sp = nullptr;
   int64_t lds = 0;
   if (mx) {
-    const Scales sc(a[4], rows, d->d_in, "x_scale", true);
+    const Scales sc(call, a[4], rows, d->d_in, "x_scale", true);
     sp = static_cast<const uint8_t *>(sc.p);
     lds = sc.ld;
   }
-  const Mat y(a[3], P, d->d_out, "y");
-  lora_stream_t s = stream(a[5]);
+  const Mat y(call, a[3], P, d->d_out, "y");
+  call.uses(tensor(a[6], "the experts' weights"), "the experts' weights");
+  if (a[7] != Py_None) call.uses(tensor(a[7], "the metadata"), "the metadata");
+  lora_stream_t s = call.stream(a[5]);
   return unlocked([&] { return lora_moe_product(d, m, x.p, mx ? 2 * x.ld : x.ld, sp, lds, y.p, y.ld, y.dtype, s); });
 }
 
 // (x, codes, scales, stream), (y, codes, scales, stream): rows of x or y to the 4-bit format, or from it
 template <bool kTo> int mx4(PyObject *const *a) {
+  Call call;
   const int64_t rows = rows_of(a[0], kTo ? "x" : "y"), cols = rows_of(a[0], kTo ? "x" : "y", 1);
-  const Mat m(a[0], rows, cols, kTo ? "x" : "y"), c(a[1], rows, cols / 2, "codes", true);
-  const Scales sc(a[2], rows, cols, "scales");
-  lora_stream_t s = stream(a[3]);
+  const Mat m(call, a[0], rows, cols, kTo ? "x" : "y"), c(call, a[1], rows, cols / 2, "codes", true);
+  const Scales sc(call, a[2], rows, cols, "scales");
+  lora_stream_t s = call.stream(a[3]);
   const int32_t n = narrow(cols, "columns");
   uint8_t *cp = static_cast<uint8_t *>(c.p), *sp = static_cast<uint8_t *>(sc.p);
   return unlocked([&] {
@@ -189,21 +231,23 @@ template <bool kTo> int mx4(PyObject *const *a) {
 
 // (y13, h, pair_slot or None, stream)
 int moe_act(PyObject *const *a) {
+  Call call;
   const int64_t P = rows_of(a[1], "h"), inter = rows_of(a[1], "h", 1);
-  const Mat y(a[0], P, 2 * inter, "y13"), h(a[1], P, inter, "h");
-  const int32_t *slot = vec<int32_t>(a[2], P, "pair_slot");
-  lora_stream_t s = stream(a[3]);
+  const Mat y(call, a[0], P, 2 * inter, "y13"), h(call, a[1], P, inter, "h");
+  const int32_t *slot = vec<int32_t>(call, a[2], P, "pair_slot");
+  lora_stream_t s = call.stream(a[3]);
   const int32_t p32 = narrow(P, "pairs"), i32 = narrow(inter, "columns");
   return unlocked([&] { return lora_moe_act(y.p, y.ld, y.dtype, slot, p32, i32, h.p, h.ld, h.dtype, s); });
 }
 
 // (y13, codes, scales, pair_slot or None, stream)
 int moe_act_mx4(PyObject *const *a) {
+  Call call;
   const int64_t P = rows_of(a[0], "y13"), inter = rows_of(a[0], "y13", 1) / 2;
-  const Mat y(a[0], P, 2 * inter, "y13"), c(a[1], P, inter / 2, "codes", true);
-  const Scales sc(a[2], P, inter, "scales");
-  const int32_t *slot = vec<int32_t>(a[3], P, "pair_slot");
-  lora_stream_t s = stream(a[4]);
+  const Mat y(call, a[0], P, 2 * inter, "y13"), c(call, a[1], P, inter / 2, "codes", true);
+  const Scales sc(call, a[2], P, inter, "scales");
+  const int32_t *slot = vec<int32_t>(call, a[3], P, "pair_slot");
+  lora_stream_t s = call.stream(a[4]);
   const int32_t p32 = narrow(P, "pairs"), i32 = narrow(inter, "columns");
   return unlocked([&] {
     return lora_moe_act_mx(y.p, y.ld, y.dtype, slot, p32, i32, static_cast<uint8_t *>(c.p), c.ld,
@@ -213,12 +257,13 @@ int moe_act_mx4(PyObject *const *a) {
 
 // (y, topk_w, out, pair_slot or None, accumulate, stream)
 int moe_combine(PyObject *const *a) {
+  Call call;
   const int64_t T = rows_of(a[1], "topk_w"), topk = rows_of(a[1], "topk_w", 1), n = rows_of(a[2], "out", 1);
-  const Mat y(a[0], T * topk, n, "y"), out(a[2], T, n, "out");
-  const float *w = vec<float>(a[1], T * topk, "topk_w");
-  const int32_t *slot = vec<int32_t>(a[3], T * topk, "pair_slot");
+  const Mat y(call, a[0], T * topk, n, "y"), out(call, a[2], T, n, "out");
+  const float *w = vec<float>(call, a[1], T * topk, "topk_w");
+  const int32_t *slot = vec<int32_t>(call, a[3], T * topk, "pair_slot");
   const bool accumulate = truth(a[4]);
-  lora_stream_t s = stream(a[5]);
+  lora_stream_t s = call.stream(a[5]);
   const int32_t t32 = narrow(T, "tokens"), k32 = narrow(topk, "choices"), n32 = narrow(n, "columns");
   return unlocked([&] {
     return lora_moe_combine(y.p, y.ld, y.dtype, w, slot, t32, k32, n32, out.p, out.ld, out.dtype, accumulate, s);
@@ -242,7 +287,7 @@ template <int (*F)(PyObject *const *), int N> PyMethodDef method(const char *nam
 }
 
 PyMethodDef methods[] = {method<moe_route, 11>("moe_route"),
-                         method<moe_product, 6>("moe_product"),
+                         method<moe_product, 8>("moe_product"),
                          method<mx4<true>, 4>("mx4_quantize"),
                          method<mx4<false>, 4>("mx4_dequantize"),
                          method<moe_act, 4>("moe_act"),

@@ -65,3 +65,25 @@ def test_x_scale_rows_are_whole_in_memory(ra):
     for s in short:
         with pytest.raises(ValueError, match="x_scale: expected rows of 16 bytes"):
             ra.moe_product(w, Meta(ra, s.size(0)), z(s.size(0), 48, **U8), z(s.size(0), 16), x_scale=s)
+
+
+def test_tensors_on_the_cpu_are_refused(ra):
+    codes, scales = z(3, 32, **U8), z(3, 16, **U8)
+    ids, w, slot = z(3, 2, **I32), z(3, 2), z(6, **I32)
+    for call in (lambda: ra.moe_route(z(3, 8), 2, topk_ids=ids, topk_w=w, pair_slot=slot),
+                 lambda: ra.mx4_quantize(z(3, 64), codes, scales),
+                 lambda: ra.mx4_dequantize(codes, scales, z(3, 64)),
+                 lambda: ra.moe_act(z(6, 32), z(6, 16), pair_slot=slot),
+                 lambda: ra.moe_act_mx4(z(3, 128), codes, scales),
+                 lambda: ra.moe_combine(z(6, 16), w, z(3, 16), pair_slot=slot),
+                 lambda: ra.moe_product(ra.ExpertWeights(z(2, 16, 32)), Meta(ra, 4), z(4, 32), z(4, 16)),
+                 lambda: ra.ExpertWeights(z(2, 16, 16, **U8), z(2, 16, 16, **U8))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+
+
+def test_shapes_and_types_are_named_before_the_device(ra):
+    with pytest.raises(TypeError, match="h: expected bf16 or fp32"):
+        ra.moe_act(z(4, 32), z(4, 16, dtype=torch.float16))
+    with pytest.raises(ValueError, match="pair_slot: expected 4"):
+        ra.moe_act(z(4, 32), z(4, 16), pair_slot=z(3, **I32))
