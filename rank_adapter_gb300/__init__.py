@@ -12,7 +12,8 @@ Low-level functions carry the C names and return the C status codes
 ``lora_meta_tiles_bytes``, ``lora_query_status``, ``lora_strerror``,
 ``lora_last_cuda_error``). ``SlotTable`` and ``TokenMeta`` own torch buffers
 laid out as the ABI wants and call those functions; ``shrink`` / ``expand``
-raise ``LoraError`` on a non-zero status.
+raise ``LoraError`` on a non-zero status. A call with ``stream=`` runs and
+allocates on that stream; the caller orders it after whatever wrote its inputs.
 
 The mixture-of-experts layer around its LoRA: ``moe_route``, ``ExpertWeights`` and
 ``moe_product``, ``mx4_quantize`` / ``mx4_dequantize``, ``moe_act`` / ``moe_act_mx4`` and
@@ -184,6 +185,36 @@ def _stream(stream) -> Optional[int]:
             _current = (torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice)
         return torch.cuda.current_stream().cuda_stream
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _side(stream, device):
+    """``stream`` as a torch stream, or None where it is the current one (or not given)."""
+    import torch
+    if stream is None or torch.device(device).type != "cuda":
+        return None
+    raw = _stream(stream)
+    if raw == torch.cuda.current_stream(device).cuda_stream:
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+
+
+def _allocate(stream, device, make, returned=True):
+    """make(), a tensor or a tuple of them, for a call on ``stream``: from that stream's memory, since a block of the
+    current stream's may still be in use there. Tensors that are ``returned`` are not reused before the current stream,
+    where the caller may read them, has reached the point at which they are dropped."""
+    side = _side(stream, device)
+    if side is None:
+        return make()
+    import torch
+    with torch.cuda.stream(side):
+        out = make()
+    if returned:
+        here = torch.cuda.current_stream(device)
+        for t in out if isinstance(out, tuple) else (out,):
+            t.record_stream(here)
+    return out
 
 
 def _ptrs(seq, n=LORA_MAX_SLICES):
@@ -452,9 +483,10 @@ def workspace(table: SlotTable, max_tokens: int, kind: int = LORA_AUTO, device="
     return torch.empty((nb + 15) // 16 * 4, dtype=torch.float32, device=device) if nb else None
 
 
-def _ws_args(table, meta, kind, ws):
+def _ws_args(table, meta, kind, ws, stream):
     if ws is None:
-        ws = workspace(table, meta.c.num_tokens, kind)
+        ws = (workspace(table, meta.c.num_tokens, kind) if stream is None else
+              _allocate(stream, "cuda", lambda: workspace(table, meta.c.num_tokens, kind), returned=False))
     if ws is None:
         return 0, 0, None
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
@@ -465,7 +497,7 @@ def shrink(table: SlotTable, meta: TokenMeta, x, buf, kind: int = LORA_AUTO, str
     """buf[s, t, :] = scale * x[t] @ A_s[slot t] for LoRA tokens (see lora_shrink).
 
     ws: scratch from workspace(); allocated per call when omitted."""
-    wsp, wsb, _keep = _ws_args(table, meta, kind, ws)
+    wsp, wsb, _keep = _ws_args(table, meta, kind, ws, stream)
     check(lora_shrink(table.desc, meta.c, x.data_ptr(), x.stride(0), buf.data_ptr(), kind, wsp, wsb, stream),
           "lora_shrink")
 
@@ -481,7 +513,8 @@ def moe_pair_slots(token_slot, topk_ids, num_loras: int, num_experts: int, local
     import torch
     T, topk = int(topk_ids.shape[0]), int(topk_ids.shape[1])
     if pair_slot is None:
-        pair_slot = torch.empty(T * topk, dtype=torch.int32, device=topk_ids.device)
+        pair_slot = _allocate(stream, topk_ids.device,
+                              lambda: torch.empty(T * topk, dtype=torch.int32, device=topk_ids.device))
     check(lora_moe_pair_slots(token_slot.data_ptr() if T else 0, topk_ids.data_ptr() if T else 0, T, topk,
                               num_loras, num_experts, local_experts,
                               expert_map.data_ptr() if expert_map is not None else 0,
@@ -504,7 +537,7 @@ def apply(table: SlotTable, meta: TokenMeta, x, y, buf=None, kind: int = LORA_AU
     ws: scratch from workspace(); allocated per call when omitted."""
     import torch
     ydt = LORA_BF16 if y.dtype == torch.bfloat16 else LORA_F32
-    wsp, wsb, _keep = _ws_args(table, meta, kind, ws)
+    wsp, wsb, _keep = _ws_args(table, meta, kind, ws, stream)
     check(lora_apply(table.desc, meta.c, x.data_ptr(), x.stride(0), buf.data_ptr() if buf is not None else 0,
                      y.data_ptr(), y.stride(0), ydt, kind, wsp, wsb, stream), "lora_apply")
 
@@ -568,9 +601,13 @@ class ExpertWeights:
                 raise ValueError(f"ExpertWeights: 4-bit weights and their scales are on the current CUDA device, got {w.device} "
                                  f"and {scale.device}")
             d.dtype, d.d_in = LORA_MXFP4, 2 * w.shape[2]
-            tiles = torch.empty(lora_mx_tiles_bytes(d.num_experts, d.d_out, d.d_in), dtype=torch.uint8, device=w.device)
+            nb = lora_mx_tiles_bytes(d.num_experts, d.d_out, d.d_in)
+            tiles = _allocate(stream, w.device, lambda: torch.empty(nb, dtype=torch.uint8, device=w.device))
             check(lora_mx_tile_scales(scale.data_ptr(), scale.shape[2], d.num_experts, d.d_out, d.d_in,
                                       tiles.data_ptr(), stream), "lora_mx_tile_scales")
+            side = _side(stream, w.device)
+            if side is not None:
+                scale.record_stream(side)  # the caller may drop it before the layout has run
             d.W_scale, scale = tiles.data_ptr(), tiles
         else:
             d.dtype = _dt(w)
@@ -600,11 +637,11 @@ def moe_route(logits, topk: int, score="softmax", renormalize: bool = True, scal
     ``pair_slot`` (int32 [T * topk]): when given, also receives the pairs' product slots."""
     if topk_ids is None or topk_w is None:
         import torch
-        shape = (logits.shape[0], topk)
+        new = dict(size=(logits.shape[0], topk), device=logits.device)
         if topk_ids is None:
-            topk_ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
+            topk_ids = _allocate(stream, logits.device, lambda: torch.empty(dtype=torch.int32, **new))
         if topk_w is None:
-            topk_w = torch.empty(shape, dtype=torch.float32, device=logits.device)
+            topk_w = _allocate(stream, logits.device, lambda: torch.empty(dtype=torch.float32, **new))
     st = (_binding or _native()).moe_route(logits, topk, _SCORES.get(score, score), renormalize, scale, expert_map,
                                            local_experts, topk_ids, topk_w, pair_slot, _raw(stream))
     if st:
@@ -633,7 +670,7 @@ def mx4_buffers(rows: int, cols: int, device="cuda"):
 def mx4_quantize(x, codes=None, scales=None, stream=None):
     """(codes, scales) of the rows of x [rows, cols] in the microscaled 4-bit format (see lora_mx_quantize)."""
     if codes is None or scales is None:
-        c, s = mx4_buffers(x.shape[0], x.shape[1], x.device)
+        c, s = _allocate(stream, x.device, lambda: mx4_buffers(x.shape[0], x.shape[1], x.device))
         codes, scales = c if codes is None else codes, s if scales is None else scales
     st = (_binding or _native()).mx4_quantize(x, codes, scales, _raw(stream))
     if st:
