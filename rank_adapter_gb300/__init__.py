@@ -12,7 +12,7 @@ Low-level functions carry the C names and return the C status codes
 ``lora_meta_tiles_bytes``, ``lora_query_status``, ``lora_strerror``,
 ``lora_last_cuda_error``). ``SlotTable`` and ``TokenMeta`` own torch buffers
 laid out as the ABI wants and call those functions; ``shrink`` / ``expand``
-raise ``LoraError`` on a non-zero status. A call with ``stream=`` runs and
+raise ``LoraError`` on a non-zero status. A call with ``stream=`` runs, copies and
 allocates on that stream; the caller orders it after whatever wrote its inputs.
 
 The mixture-of-experts layer around its LoRA: ``moe_route``, ``ExpertWeights`` and
@@ -457,7 +457,15 @@ class TokenMeta:
             n = int(token_slot.numel())
             self.set_num_tokens(n)
             if n:
-                self.token_slot[:n].copy_(token_slot, non_blocking=True)
+                side = _side(stream, self.token_slot.device)
+                if side is None:
+                    self.token_slot[:n].copy_(token_slot, non_blocking=True)
+                else:
+                    import torch
+                    with torch.cuda.stream(side):  # where the metadata kernel runs
+                        self.token_slot[:n].copy_(token_slot, non_blocking=True)
+                    if token_slot.is_cuda:
+                        token_slot.record_stream(side)
         if unshared:
             check(lora_prepare_meta_unshared(self.c, stream), "lora_prepare_meta_unshared")
         else:

@@ -1,4 +1,4 @@
-"""A call with ``stream=`` allocates and keeps for that stream: what it returns is not memory that the
+"""A call with ``stream=`` allocates, copies and keeps for that stream: what it returns is not memory that the
 current stream may still be using, nor is memory it reads given back before it has been read."""
 import pytest
 import torch
@@ -76,6 +76,19 @@ def test_expert_weights_scales_outlive_their_layout(lib):
     assert again.data_ptr() != p
     torch.cuda.synchronize()
     assert e.scale is not None
+
+
+def test_metadata_copies_on_the_stream_it_is_prepared_on(lib):
+    s = torch.cuda.Stream()
+    meta = lib.TokenMeta(300, 4)
+    slot = torch.arange(300, dtype=torch.int32, device="cuda") % 4
+    meta.prepare(torch.zeros_like(slot), stream=s)     # the kernel is loaded, which waits for the device
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                     # the current stream is busy with something else
+    meta.prepare(slot, stream=s)
+    s.synchronize()
+    assert meta.seg_count[1:3].tolist() == [75, 75]
+    assert torch.equal(meta.sorted_rows.sort().values, torch.arange(300, dtype=torch.int32, device="cuda"))
 
 
 def test_a_calls_own_workspace_is_the_streams(lib, monkeypatch):
