@@ -16,7 +16,7 @@ namespace {
 // weights need one or two warp sums. A long batch is bound by the rounds'
 // instructions: 16-bit logits carry their expert in the key's low half, so
 // that one reduction a round gives both, and lanes with few keys sort them first
-// (16381 tokens of 256 experts, top 8: 8.8 us;
+// (16381 tokens of 256 experts, top 8: 8.8 us; before that
 // unsorted 11.5 us; with separate reductions, as for fp32 logits, 15.1 us).
 
 constexpr int kRouteWarps = 4;
@@ -181,8 +181,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(RouteArgs a
     const bool chosen = lane < a.topk, live = chosen && Keys::numbered(mine);
     float w = 0.f;
     if (live) {
+      // A sigmoid below e^-18 is its exponential (1 + e^v is 1 in fp32), which
+      // keeps it a number down to -103. Where the first choice is one, all are:
+      // renormalised weights are then a softmax's, whose common factor cancels,
+      // however low the logits are.
       const float v = Keys::value(mine);
-      w = a.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - Keys::value(first));
+      if (!a.sigmoid || (a.renorm && first < order_key(-18.f))) w = expf(v - Keys::value(first));
+      else if (v < -18.f) w = expf(v);
+      else w = 1.f / (1.f + expf(-v));
     }
     if (a.renorm) {
       total = w;
