@@ -475,7 +475,9 @@ size_t lora_mx_tiles_bytes(int32_t num_experts, int32_t d_out, int32_t d_in);
  * The gated activation between w13 and w2, for every pair with pair_slot > 0
  * (every row when pair_slot is NULL; other rows are left alone):
  *   h[p, i] = silu(y13[p, i]) * y13[p, inter + i]        silu(g) = g / (1 + exp(-g))
- * in fp32, rounded once.
+ * in fp32, rounded once. For a bf16 h silu comes from an approximate exponential
+ * and reciprocal, within (10 + |g|) * 2^-23 of its value (below g = -87, where it
+ * nears fp32's smallest numbers, within |g| * 2^-147 besides).
  *   y13: device, [num_pairs, 2 * inter], row stride ldy elements, LORA_F32 or
  *        LORA_BF16; inter a positive multiple of 8
  *   h:   device, [num_pairs, inter], row stride ldh elements, LORA_F32 or LORA_BF16
