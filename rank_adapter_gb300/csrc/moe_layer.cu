@@ -243,8 +243,9 @@ struct ActArgs {
 // its exponent, its square, the reciprocal within 1 ulp, three roundings. The
 // square reaches the subnormal numbers, so the power need not: no scaling of its
 // own (with CUDA's fast exponential and a reciprocal 65.5 us for 32744 rows of
-// 2048, so 59.0). An fp32 result takes the exact ones, which would bind a bf16
-// one by instructions (88.5 us for those rows, 66.9 with the fast ones then).
+// 2048, as here 59.0). An fp32 result takes the exact ones; for a bf16 one they bound
+// the kernel by instructions (88.5 us where CUDA's fast ones took 66.9, at an
+// earlier stage).
 template <bool kFast> __device__ __forceinline__ float silu(float g) {
   if constexpr (kFast) {
     float h, r;
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kThreads) moe_act_mx_kernel(ActArgs a) {
 // rows of up to kAhead choices are requested before the first is used. With
 // tokens enough for every SM a CTA walks all columns of its tokens, so that
 // the token's slots and weights come from L1 after the first (32744 rows of
-// 7168: 84.0 us, 0.94 of the measured copy rate; with CTAs of 256 threads 85.4
+// 7168: 83.8 us, 0.93 of the measured copy rate; with CTAs of 256 threads 85.4
 // us, and with one of those for each 2048 columns 94.8 us).
 constexpr int kCombineThreads = 128;
 

@@ -23,10 +23,11 @@
 //
 // What bounds it (w2 prefill: 32744 rows of 16 experts, 2048 by 7168; w13:
 // 7168 by 4096): few rows, the weights' bytes (7.0 to 7.5 TB/s); bf16 prefill
-// the tensor pipe, 93 % active, and the power cap (w2 521 us, 1.84 PFLOP/s,
-// in short runs); 4-bit prefill no single unit (tensor pipe 53 % active, shared
-// memory 63 % busy) but the order of scale copies and MMAs in the tensor pipe
-// (w13 370 us, 5.2 PFLOP/s); one or two experts' few tiles the pipeline's round
+// the tensor pipe, 96 % active, and the power cap (w2 in short runs 512 us, 1.88
+// PFLOP/s, sustained 598 to 635 us, 1.5 to 1.6 PFLOP/s); 4-bit prefill no single
+// unit (tensor pipe 54 % active, shared memory 64 % busy) but the order of scale
+// copies and MMAs in the tensor pipe (w13 in short runs 367 us, 5.2 PFLOP/s,
+// sustained 381 to 388 us); one or two experts' few tiles the pipeline's round
 // trip, about 0.2 us a stage.
 #include <atomic>
 
