@@ -65,8 +65,10 @@ typedef enum {
   LORA_EBADSLOT = 6,      /* lora_query_status: some token slot ids were out of range */
   LORA_EDEVICE = 7,       /* lora_query_status: a kernel gave up waiting on its own pipeline
                              (a fault it avoided); outputs since lora_prepare_meta are invalid */
-  LORA_EBADTOKEN = 8      /* lora_query_status: lora_embed_shrink met token ids outside the
+  LORA_EBADTOKEN = 8,     /* lora_query_status: lora_embed_shrink met token ids outside the
                              vocabulary; those rows got no delta, the rest are valid */
+  LORA_EBADSEQ = 9        /* lora_query_seqs: some sequences' rows, lengths or page ids were
+                             out of range; those got no attention, or zeros for keys */
 } lora_status;
 
 /* LORA_MXFP4 (experts' weights and their inputs only): the microscaled 4-bit
@@ -105,6 +107,10 @@ typedef enum { LORA_AUTO = 0, LORA_BGMV = 1, LORA_SGMV = 2, LORA_MIXED = 3 } lor
 #define LORA_MAX_ROUTE_TOPK 32     /* lora_moe_route: choices of a token */
 #define LORA_MAX_EXPERT_DIM (1 << 24)  /* d_in and d_out of an expert's projection */
 #define LORA_MX_BLOCK 32           /* elements that share a scale in the 4-bit format */
+#define LORA_MAX_SEQS 16384        /* lora_seqs: sequences of a step */
+#define LORA_MAX_HEADS 1024        /* lora_seqs: query heads */
+#define LORA_MAX_HEAD_DIM 256      /* lora_seqs: elements of a head */
+#define LORA_MAX_KV_LEN (1 << 24)  /* lora_seqs: keys of a sequence */
 #define LORA_SGMV_MIN_ROWS 32      /* AUTO threshold: segment rows routed to SGMV */
 #define LORA_SGMV_TILE_M 128       /* rows per SGMV tile (work-list granularity) */
 #define LORA_AUTO_SGMV_MIN_TOKENS 1024  /* AUTO: smaller batches run all on BGMV */
@@ -509,6 +515,163 @@ int lora_moe_act_mx(const void *y13, int64_t ldy, int32_t y_dtype, const int32_t
 int lora_moe_combine(const void *y, int64_t ldy, int32_t y_dtype, const float *topk_w, const int32_t *pair_slot,
                      int32_t num_tokens, int32_t topk, int32_t n, void *out, int64_t ldo, int32_t out_dtype,
                      int32_t accumulate, lora_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The attention between a layer's qkv LoRA and its o LoRA, and the cache it
+ * reads. The multi-LoRA pages take the attention's output as o_proj's input;
+ * the calls below compute it from the packed qkv rows that lora_apply leaves,
+ * so that a layer runs as
+ *   lora_apply (qkv) -> lora_kv_write -> lora_attn_paged -> lora_apply (o)
+ * or, for prompts without anything in the cache, with lora_attn_prompt. One
+ * lora_prepare_seqs a step serves all layers of one geometry. Rows are the
+ * batch's tokens, those of a sequence next to each other; every kernel waits
+ * for its predecessor before it reads anything.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * The sequences of a step, as layers of one geometry see them.
+ *   dtype         LORA_BF16, or LORA_F32 (accuracy runs), of q, k, v, the
+ *                 cache and the output
+ *   num_heads, num_kv_heads, head_dim
+ *                 query heads (up to LORA_MAX_HEADS), key-value heads that
+ *                 divide them (query head h reads key-value head h /
+ *                 (num_heads / num_kv_heads)), elements of a head: a multiple
+ *                 of 8 up to LORA_MAX_HEAD_DIM. bf16 heads of 64 and 128 with
+ *                 up to 128 query heads a key-value head run on the tensor
+ *                 cores, others on the CUDA cores.
+ *   causal        non-zero: a row sees the keys up to its own position
+ *   scale         of the scores, positive and finite (1 / sqrt(head_dim))
+ *   q_start       device int32 [num_seqs + 1]: sequence b has the rows
+ *                 [q_start[b], q_start[b + 1]); rows behind the last
+ *                 sequence's are left alone
+ *   kv_len        device int32 [num_seqs]: keys of a sequence, its own rows'
+ *                 among them as the last; NULL: its own rows only
+ *   num_seqs, num_tokens
+ *                 up to LORA_MAX_SEQS; rows of the batch
+ *   page_size, max_pages, block_table, ld_table
+ *                 for the cache (else 0 and NULL): keys of a page, a power of
+ *                 two in [8, 1024]; pages of a sequence at most; device int32
+ *                 [num_seqs, max_pages] with row stride ld_table: the page
+ *                 that holds keys [i * page_size, (i + 1) * page_size). Read
+ *                 by lora_kv_write and lora_attn_paged, up to kv_len only.
+ *   plan          device, at least lora_seqs_plan_bytes() bytes, 16-byte
+ *                 aligned; its layout is private to the library
+ * The library only reads this struct. q_start and kv_len are read by
+ * lora_prepare_seqs alone; the other calls take what it has put in the plan,
+ * with the same struct but for a block_table.
+ */
+typedef struct {
+  int32_t dtype;
+  int32_t num_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t causal;
+  float scale;
+  const int32_t *q_start;
+  const int32_t *kv_len;
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t page_size;
+  int32_t max_pages;
+  const int32_t *block_table;
+  int64_t ld_table;
+  void *plan;
+  size_t plan_bytes;
+} lora_seqs;
+
+/*
+ * One layer's keys and values: num_pages pages of page_size keys of
+ * num_kv_heads heads of head_dim elements. Element d of a key's head is at
+ * page * k_page + key * k_row + head * k_head + d (v likewise, strides in
+ * elements), so that any order of pages, keys and heads will do; the pages,
+ * keys and heads of k, and those of v, do not overlap.
+ * k and v are 16-byte aligned device pointers, strides are positive and
+ * multiples of 16 bytes.
+ */
+typedef struct {
+  void *k, *v;
+  int64_t k_page, k_row, k_head;
+  int64_t v_page, v_row, v_head;
+  int32_t num_pages;
+} lora_kv_cache;
+
+/* Bytes of the plan for up to this many sequences and rows; 0 for an invalid geometry. */
+size_t lora_seqs_plan_bytes(const lora_seqs *seqs);
+
+/*
+ * Check the sequences and cut their attention into work of even size: long
+ * rows of keys are split, and the parts joined when all are done. A sequence
+ * whose rows are not within [0, num_tokens], or whose keys are negative, more
+ * than max_pages * page_size (where there is a cache) or more than
+ * LORA_MAX_KV_LEN, is treated as empty and counted (lora_query_seqs). One call
+ * a step serves all layers of the geometry.
+ * Errors: null pointers, a plan that is too small, a head_dim that is no
+ * multiple of 8, kv heads that do not divide the heads, a scale that is not
+ * positive and finite, an invalid page_size -> LORA_EINVAL; counts outside
+ * their limits -> LORA_ERANGE; misaligned arrays -> LORA_EALIGN.
+ */
+int lora_prepare_seqs(const lora_seqs *seqs, lora_stream_t stream);
+
+/*
+ * The rows' keys and values into the cache: row i of sequence b, of n rows and
+ * L keys, is key p = L - n + i, at key p % page_size of page
+ * block_table[b, p / page_size]. Rows without a position (L < n) and rows
+ * whose page id is outside [0, num_pages) are not written; the latter are
+ * reported by lora_query_seqs. Sequences that write may not share the pages
+ * they write to (which row stays is then not defined).
+ *   k, v: device, [num_tokens, num_kv_heads * head_dim], row strides ldk, ldv
+ *         elements (column ranges of the packed qkv rows, say)
+ */
+int lora_kv_write(const lora_seqs *seqs, const lora_kv_cache *cache, const void *k, int64_t ldk, const void *v,
+                  int64_t ldv, lora_stream_t stream);
+
+/*
+ * Attention of every sequence's rows over its own rows (a plan with kv_len
+ * NULL): for row i of a sequence and every query head h,
+ *   s_j = scale * q . k_j     over the keys j it sees (causal: j <= i)
+ *   out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  m = max_j s_j
+ *   lse = m + log(sum_j exp(s_j - m))
+ * A row that sees no key gets out = 0 and lse = -infinity. Scores, maxima and
+ * sums are fp32; on the tensor cores a weight is rounded to bf16 before it
+ * multiplies v (not in the sum), which is off by at most 2^-8 of it; out is
+ * rounded once. Keys and values that a row does not see do not reach it, NaN
+ * and infinity among them. Results do not depend on other sequences' values
+ * and repeat bitwise on the same plan and device.
+ *   q, out: device, [num_tokens, num_heads * head_dim], row strides ldq, ldo
+ *   k, v:   device, [num_tokens, num_kv_heads * head_dim], row strides ldk, ldv
+ *   lse:    device fp32 [num_tokens, num_heads] contiguous, or NULL
+ *   ws:     device scratch of lora_attn_workspace_bytes(seqs), 16-byte aligned.
+ *           It needs no initialisation; calls that share it must not overlap
+ *           in time.
+ * out must not overlap the inputs. Errors: null pointers, strides below a
+ * row's length, a plan of another kind, too little scratch -> LORA_EINVAL;
+ * pointers and row strides that are not multiples of 16 bytes -> LORA_EALIGN.
+ */
+int lora_attn_prompt(const lora_seqs *seqs, const void *q, int64_t ldq, const void *k, int64_t ldk, const void *v,
+                     int64_t ldv, void *out, int64_t ldo, float *lse, void *ws, size_t ws_bytes, lora_stream_t stream);
+
+/*
+ * Attention of every sequence's rows (one token, or a chunk of them) over its
+ * keys in the cache, the rows' own among them (lora_kv_write before). Row i of
+ * n, at position p = kv_len - n + i, sees keys [0, p] (causal) or all. Keys of
+ * a page id outside [0, num_pages) count as zeros, and are reported by
+ * lora_query_seqs. Slots of a page behind kv_len may hold anything.
+ * Otherwise as lora_attn_prompt.
+ */
+int lora_attn_paged(const lora_seqs *seqs, const lora_kv_cache *cache, const void *q, int64_t ldq, void *out,
+                    int64_t ldo, float *lse, void *ws, size_t ws_bytes, lora_stream_t stream);
+
+/* Scratch bytes of lora_attn_prompt and lora_attn_paged on the current device; 0 for an invalid geometry. */
+size_t lora_attn_workspace_bytes(const lora_seqs *seqs);
+
+/*
+ * Synchronise `stream`, copy the number of sequences that the last
+ * lora_prepare_seqs treated as empty to *out (host), and return LORA_EDEVICE
+ * if an attention kernel since then gave up waiting on its own pipeline, else
+ * LORA_EBADSEQ if *out is not 0 or a page id was outside the cache, else
+ * LORA_OK.
+ */
+int lora_query_seqs(const lora_seqs *seqs, int32_t *out, lora_stream_t stream);
 
 /*
  * Synchronise `stream`, copy meta->status to *out (host) and return

@@ -17,7 +17,9 @@ allocates on that stream; the caller orders it after whatever wrote its inputs.
 
 The mixture-of-experts layer around its LoRA: ``moe_route``, ``ExpertWeights`` and
 ``moe_product``, ``mx4_quantize`` / ``mx4_dequantize``, ``moe_act`` / ``moe_act_mx4`` and
-``moe_combine`` (``lora_moe_*`` and ``lora_mx_*`` in the header). Their tensor forms are
+``moe_combine`` (``lora_moe_*`` and ``lora_mx_*`` in the header). The attention between the qkv
+and the o adapter: ``Attention`` (a geometry), ``SeqMeta`` (a step's sequences), ``KVCache``,
+``kv_write``, ``attn_prompt`` and ``attn_paged``. The tensor forms of both are
 marshalled natively (``binding/moe_binding.cpp``), which raises for tensors of the wrong
 shape or type or not on the current CUDA device; the C-named ones go through ctypes.
 """
@@ -40,6 +42,10 @@ __all__ = [
     "LORA_MAX_EXPERT_DIM", "LORA_MX_BLOCK",
     "lora_moe_route", "lora_moe_product", "lora_mx_quantize", "lora_mx_dequantize",
     "lora_mx_tile_scales", "lora_mx_tiles_bytes", "lora_moe_act", "lora_moe_act_mx",
+    "LORA_EBADSEQ", "LORA_MAX_SEQS", "LORA_MAX_HEADS", "LORA_MAX_HEAD_DIM", "LORA_MAX_KV_LEN",
+    "lora_seqs_plan_bytes", "lora_prepare_seqs", "lora_kv_write", "lora_attn_prompt", "lora_attn_paged",
+    "lora_attn_workspace_bytes", "lora_query_seqs", "SeqsDesc", "KVCacheDesc", "Attention", "SeqMeta", "KVCache",
+    "kv_write", "attn_prompt", "attn_paged", "attn_workspace",
     "lora_moe_combine", "ExpertDesc", "ExpertWeights", "moe_route", "moe_product", "mx4_buffers", "mx4_quantize",
     "mx4_dequantize", "moe_act", "moe_act_mx4", "moe_combine",
     "lora_workspace_bytes", "lora_meta_tiles_bytes", "lora_query_status", "lora_probe_bounded_wait", "lora_strerror",
@@ -47,7 +53,7 @@ __all__ = [
 ]
 
 (LORA_OK, LORA_EINVAL, LORA_ERANGE, LORA_EALIGN, LORA_EUNSUPPORTED, LORA_ECUDA, LORA_EBADSLOT, LORA_EDEVICE,
- LORA_EBADTOKEN) = range(9)
+ LORA_EBADTOKEN, LORA_EBADSEQ) = range(10)
 LORA_F32, LORA_BF16 = 0, 1
 LORA_AUTO, LORA_BGMV, LORA_SGMV, LORA_MIXED = 0, 1, 2, 3
 LORA_MXFP4 = 2                                  # experts' weights and inputs only
@@ -60,6 +66,10 @@ LORA_MAX_SLICES = 4
 LORA_MAX_NUM_SLOTS = 1024
 LORA_MAX_RANK = 128
 LORA_MAX_TOKENS = 1 << 24
+LORA_MAX_SEQS = 16384
+LORA_MAX_HEADS = 1024
+LORA_MAX_HEAD_DIM = 256
+LORA_MAX_KV_LEN = 1 << 24
 LORA_SGMV_MIN_ROWS = 32
 LORA_SGMV_TILE_M = 128
 LORA_AUTO_SGMV_MIN_TOKENS = 1024
@@ -113,6 +123,24 @@ class ExpertDesc(ctypes.Structure):
 
 
 _i64 = ctypes.c_int64
+
+
+class SeqsDesc(ctypes.Structure):
+    """lora_seqs: a step's sequences as layers of one attention geometry see them (device pointers)."""
+    _fields_ = [
+        ("dtype", _i32), ("num_heads", _i32), ("num_kv_heads", _i32), ("head_dim", _i32), ("causal", _i32),
+        ("scale", ctypes.c_float), ("q_start", _vp), ("kv_len", _vp), ("num_seqs", _i32), ("num_tokens", _i32),
+        ("page_size", _i32), ("max_pages", _i32), ("block_table", _vp), ("ld_table", _i64),
+        ("plan", _vp), ("plan_bytes", ctypes.c_size_t),
+    ]
+
+
+class KVCacheDesc(ctypes.Structure):
+    """lora_kv_cache: one layer's pages of keys and values (device pointers, strides in elements)."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_page", _i64), ("k_row", _i64), ("k_head", _i64), ("v_page", _i64),
+                ("v_row", _i64), ("v_head", _i64), ("num_pages", _i32)]
+
+
 _P = ctypes.POINTER
 _sig = {
     "lora_set_slot": (_i32, [_P(LayerDesc), _i32, _i32, ctypes.c_float, _P(_vp), _P(_vp), _vp]),
@@ -141,6 +169,13 @@ _sig = {
     "lora_moe_act": (_i32, [_vp, _i64, _i32, _vp, _i32, _i32, _vp, _i64, _i32, _vp]),
     "lora_moe_act_mx": (_i32, [_vp, _i64, _i32, _vp, _i32, _i32, _vp, _i64, _vp, _i64, _vp]),
     "lora_moe_combine": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _i64, _i32, _i32, _vp]),
+    "lora_seqs_plan_bytes": (ctypes.c_size_t, [_P(SeqsDesc)]),
+    "lora_prepare_seqs": (_i32, [_P(SeqsDesc), _vp]),
+    "lora_kv_write": (_i32, [_P(SeqsDesc), _P(KVCacheDesc), _vp, _i64, _vp, _i64, _vp]),
+    "lora_attn_prompt": (_i32, [_P(SeqsDesc), _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, ctypes.c_size_t, _vp]),
+    "lora_attn_paged": (_i32, [_P(SeqsDesc), _P(KVCacheDesc), _vp, _i64, _vp, _i64, _vp, _vp, ctypes.c_size_t, _vp]),
+    "lora_attn_workspace_bytes": (ctypes.c_size_t, [_P(SeqsDesc)]),
+    "lora_query_seqs": (_i32, [_P(SeqsDesc), _P(_i32), _vp]),
     "lora_strerror": (ctypes.c_char_p, [_i32]),
     "lora_last_cuda_error": (_i32, []),
     "lora_launch_count": (ctypes.c_uint64, []),
@@ -324,6 +359,44 @@ def lora_moe_combine(y: int, ldy: int, y_dtype: int, topk_w: int, pair_slot: int
                      out: int, ldo: int, out_dtype: int, accumulate: bool = False, stream=None) -> int:
     return _lib.lora_moe_combine(y, ldy, y_dtype, topk_w, pair_slot, num_tokens, topk, n,
                                  out, ldo, out_dtype, int(bool(accumulate)), _stream(stream))
+
+
+def lora_seqs_plan_bytes(seqs: SeqsDesc) -> int:
+    return int(_lib.lora_seqs_plan_bytes(ctypes.byref(seqs)))
+
+
+def lora_prepare_seqs(seqs: SeqsDesc, stream=None) -> int:
+    return _lib.lora_prepare_seqs(ctypes.byref(seqs), _stream(stream))
+
+
+def lora_kv_write(seqs: SeqsDesc, cache: KVCacheDesc, k: int, ldk: int, v: int, ldv: int, stream=None) -> int:
+    """The rows' keys and values into the pages of their sequences (see the header)."""
+    return _lib.lora_kv_write(ctypes.byref(seqs), ctypes.byref(cache), k, ldk, v, ldv, _stream(stream))
+
+
+def lora_attn_prompt(seqs: SeqsDesc, q: int, ldq: int, k: int, ldk: int, v: int, ldv: int, out: int, ldo: int, lse: int,
+                     ws: int, ws_bytes: int, stream=None) -> int:
+    """Attention of every sequence's rows over its own rows (see the header)."""
+    return _lib.lora_attn_prompt(ctypes.byref(seqs), q, ldq, k, ldk, v, ldv, out, ldo, lse or None, ws, ws_bytes,
+                                 _stream(stream))
+
+
+def lora_attn_paged(seqs: SeqsDesc, cache: KVCacheDesc, q: int, ldq: int, out: int, ldo: int, lse: int, ws: int,
+                    ws_bytes: int, stream=None) -> int:
+    """Attention of every sequence's rows over its keys in the cache (see the header)."""
+    return _lib.lora_attn_paged(ctypes.byref(seqs), ctypes.byref(cache), q, ldq, out, ldo, lse or None, ws, ws_bytes,
+                                _stream(stream))
+
+
+def lora_attn_workspace_bytes(seqs: SeqsDesc) -> int:
+    return int(_lib.lora_attn_workspace_bytes(ctypes.byref(seqs)))
+
+
+def lora_query_seqs(seqs: SeqsDesc, stream=None):
+    """Returns (status_code, sequences treated as empty); synchronises the stream."""
+    out = _i32(0)
+    st = _lib.lora_query_seqs(ctypes.byref(seqs), ctypes.byref(out), _stream(stream))
+    return st, int(out.value)
 
 
 def lora_shrink_noalloc(desc: LayerDesc, meta: Meta, x: int, ldx: int, buf: int, stream=None) -> int:
@@ -715,4 +788,127 @@ def moe_combine(y, topk_w, out, pair_slot=None, accumulate: bool = False, stream
     st = (_binding or _native()).moe_combine(y, topk_w, out, pair_slot, accumulate, _raw(stream))
     if st:
         check(st, "lora_moe_combine")
+    return out
+
+
+# ----------------------------------------------------------------------------- the attention between qkv and o
+
+class Attention:
+    """An attention geometry: query heads, key-value heads that divide them, elements of a head. ``scale``: of the
+    scores, 1 / sqrt(head_dim) by default; ``causal``: a row sees the keys up to its own position."""
+
+    def __init__(self, num_heads: int, num_kv_heads: int, head_dim: int, scale: Optional[float] = None,
+                 causal: bool = True, dtype: int = LORA_BF16):
+        self.num_heads, self.num_kv_heads, self.head_dim = num_heads, num_kv_heads, head_dim
+        self.scale = head_dim ** -0.5 if scale is None else scale
+        self.causal, self.dtype = causal, dtype
+
+
+class SeqMeta:
+    """The sequences of a step, of up to ``max_seqs`` sequences and ``max_tokens`` rows, as layers of one geometry
+    see them, with the plan of their attention. ``page_size`` and ``max_pages`` (pages of a sequence at most): of the
+    cache, 0 where there is none."""
+
+    def __init__(self, att: Attention, max_tokens: int, max_seqs: int, page_size: int = 0, max_pages: int = 0,
+                 device="cuda"):
+        import torch
+        self.att, self.max_tokens, self.max_seqs = att, max_tokens, max_seqs
+        d = SeqsDesc()
+        d.dtype, d.num_heads, d.num_kv_heads, d.head_dim = att.dtype, att.num_heads, att.num_kv_heads, att.head_dim
+        d.causal, d.scale, d.page_size, d.max_pages = int(bool(att.causal)), att.scale, page_size, max_pages
+        d.num_seqs, d.num_tokens = max_seqs, max_tokens
+        d.plan_bytes = lora_seqs_plan_bytes(d)
+        if d.plan_bytes == 0:
+            raise ValueError(f"SeqMeta: invalid geometry or sizes ({att.num_heads} heads, {att.num_kv_heads} key-value heads of "
+                             f"{att.head_dim}, scale {att.scale}, {max_seqs} sequences, {max_tokens} rows)")
+        self.plan = torch.zeros(d.plan_bytes // 4, dtype=torch.int32, device=device)
+        d.plan = self.plan.data_ptr()
+        d.num_seqs = d.num_tokens = 0
+        self.q_start = self.kv_len = self.block_table = None
+        self.c, self.address = d, ctypes.addressof(d)
+
+    def prepare(self, num_tokens: int, q_start, kv_len=None, block_table=None, stream=None) -> None:
+        """Sequences of rows [q_start[b], q_start[b + 1]) of a batch of ``num_tokens`` (see lora_prepare_seqs).
+
+        ``q_start`` int32 [sequences + 1], ``kv_len`` int32 [sequences] (None: a sequence's own rows),
+        ``block_table`` int32 [sequences, max_pages]. The tensors are read where they are: q_start and kv_len by
+        this call, the table by the calls that use the cache."""
+        (_binding or _native()).prepare_seqs(self.address, num_tokens, q_start, kv_len, block_table, self.max_tokens,
+                                             self.max_seqs, self.plan)
+        self.q_start, self.kv_len, self.block_table = q_start, kv_len, block_table
+        st = lora_prepare_seqs(self.c, stream)
+        if stream is not None:
+            side = _side(stream, self.plan.device)
+            if side is not None:
+                for t in (q_start, kv_len, block_table):
+                    if t is not None:
+                        t.record_stream(side)  # the caller may drop it before the plan is made
+        if st:
+            check(st, "lora_prepare_seqs")
+
+
+class KVCache:
+    """One layer's cache: ``k`` and ``v`` [pages, page_size, key-value heads, head_dim], in any order in memory (a
+    permuted view will do) with contiguous heads' elements."""
+
+    def __init__(self, k, v):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride(3) != 1 or v.stride(3) != 1:
+            raise ValueError("KVCache: expected k and v of one shape [pages, page_size, heads, head_dim] and type with "
+                             f"contiguous elements, got {tuple(k.shape)} {k.dtype} and {tuple(v.shape)} {v.dtype}")
+        if k.device != v.device:
+            raise ValueError(f"KVCache: k on {k.device}, v on {v.device}")
+        c = KVCacheDesc()
+        c.k, c.v, c.num_pages = k.data_ptr(), v.data_ptr(), k.shape[0]
+        (c.k_page, c.k_row, c.k_head), (c.v_page, c.v_row, c.v_head) = self._strides(k), self._strides(v)
+        self.k, self.v, self.c = k, v, c
+        self.address, self.dtype = ctypes.addressof(c), _dt(k)
+
+    @staticmethod
+    def _strides(t):
+        """Strides of pages, keys and heads; where there is one only its stride means nothing, a head's size will do. Strides
+        under which elements share memory are refused."""
+        size, stride, end = t.shape, t.stride(), 1
+        for i in sorted(range(4), key=lambda i: (stride[i], i)):
+            if size[i] > 1:
+                if stride[i] < end:
+                    raise ValueError(f"KVCache: elements overlap (shape {tuple(size)}, strides {t.stride()})")
+                end = stride[i] * size[i]
+        return [stride[i] if size[i] > 1 else size[3] for i in range(3)]
+
+
+def attn_workspace(seqs: SeqMeta, device="cuda"):
+    """A caller-owned scratch tensor of lora_attn_workspace_bytes() bytes."""
+    import torch
+    return torch.empty(lora_attn_workspace_bytes(seqs.c), dtype=torch.uint8, device=device)
+
+
+def kv_write(seqs: SeqMeta, cache: KVCache, k, v, stream=None) -> None:
+    """The rows' keys and values (k, v [rows, key-value heads * head_dim]) into the cache (see lora_kv_write)."""
+    st = (_binding or _native()).kv_write(seqs.address, cache.address, k, v, cache.k, cache.v, seqs.block_table, seqs.plan,
+                                          _raw(stream))
+    if st:
+        check(st, "lora_kv_write")
+
+
+def attn_prompt(seqs: SeqMeta, q, k, v, out, lse=None, ws=None, stream=None):
+    """out = attention of q's rows over the rows of their own sequences (see lora_attn_prompt).
+
+    q, out [rows, heads * head_dim], k, v [rows, key-value heads * head_dim]; ``lse`` fp32 [rows, heads]: when given,
+    also receives the logarithms of the rows' sums. ws: scratch from attn_workspace(); allocated per call when omitted."""
+    if ws is None:
+        ws = _allocate(stream, q.device, lambda: attn_workspace(seqs, q.device), returned=False)
+    st = (_binding or _native()).attn_prompt(seqs.address, q, k, v, out, lse, ws, seqs.plan, _raw(stream))
+    if st:
+        check(st, "lora_attn_prompt")
+    return out
+
+
+def attn_paged(seqs: SeqMeta, cache: KVCache, q, out, lse=None, ws=None, stream=None):
+    """out = attention of q's rows over their sequences' keys in the cache (see lora_attn_paged); otherwise as attn_prompt."""
+    if ws is None:
+        ws = _allocate(stream, q.device, lambda: attn_workspace(seqs, q.device), returned=False)
+    st = (_binding or _native()).attn_paged(seqs.address, cache.address, q, out, lse, ws, cache.k, cache.v,
+                                            seqs.block_table, seqs.plan, _raw(stream))
+    if st:
+        check(st, "lora_attn_paged")
     return out

@@ -1,4 +1,4 @@
-// Native marshalling of the mixture-of-experts calls: reads the tensors'
+// Native marshalling of the mixture-of-experts and the attention calls: reads the tensors'
 // addresses, strides and types, checks their shapes and calls the C ABI
 // (include/lora.h) on the given or the current stream. The same through ctypes
 // takes about 4.7 us a call on the host, more than most of these kernels run
@@ -48,7 +48,7 @@ class Call {
   lora_stream_t stream(PyObject *o);
 
  private:
-  static constexpr int kMost = 8;
+  static constexpr int kMost = 12;
   struct { const at::Tensor *t; const char *name; } used_[kMost];
   int n_ = 0;
 };
@@ -270,6 +270,126 @@ int moe_combine(PyObject *const *a) {
   });
 }
 
+// ---- attention
+
+lora_seqs *seqs_at(PyObject *o) { return (lora_seqs *)(intptr_t)integer(o); }
+
+// Rows of the batch in the sequences' type, `heads` heads wide.
+Mat rows_for(Call &call, const lora_seqs *s, PyObject *o, int64_t heads, const char *name) {
+  const Mat m(call, o, s->num_tokens, heads * s->head_dim, name);
+  if (m.dtype != s->dtype) throw Refused{PyExc_TypeError, std::string(name) + ": not of the attention's type"};
+  return m;
+}
+// A page table of at least `rows` rows, and its row stride.
+int64_t table_of(Call &call, PyObject *o, int64_t rows, int64_t pages) {
+  const at::Tensor &t = tensor(o, "block_table");
+  call.uses(t, "block_table");
+  if (t.scalar_type() != at::kInt || t.dim() != 2 || t.size(0) < rows || t.size(1) < pages || (t.size(1) > 1 && t.stride(1) != 1) ||
+      (t.size(0) > 1 && t.stride(0) < t.size(1)))
+    throw Refused{PyExc_ValueError, "block_table: expected int32 [" + std::to_string(rows) + ", " + std::to_string(pages) +
+                                        "] with contiguous rows, got " + describe(t) + " " + c10::toString(t.scalar_type())};
+  return t.size(0) > 1 ? t.stride(0) : t.size(1);
+}
+// Scratch: its address and bytes.
+struct Scratch {
+  void *p;
+  size_t bytes;
+  Scratch(Call &call, PyObject *o) {
+    const at::Tensor &t = tensor(o, "ws");
+    call.uses(t, "ws");
+    if (!t.is_contiguous()) throw Refused{PyExc_ValueError, "ws: expected contiguous memory, got " + describe(t)};
+    p = t.data_ptr();
+    bytes = (size_t)t.numel() * t.element_size();
+  }
+};
+void check_cache(Call &call, const lora_seqs *s, PyObject *k, PyObject *v) {
+  for (PyObject *o : {k, v}) {
+    const at::Tensor &t = tensor(o, "cache");
+    call.uses(t, "cache");
+    if (t.dim() != 4 || t.size(1) != s->page_size || t.size(2) != s->num_kv_heads || t.size(3) != s->head_dim)
+      throw Refused{PyExc_ValueError, "cache: expected [pages, " + std::to_string(s->page_size) + ", " +
+                                          std::to_string(s->num_kv_heads) + ", " + std::to_string(s->head_dim) + "], got " + describe(t)};
+    if (t.scalar_type() != (s->dtype == LORA_BF16 ? at::kBFloat16 : at::kFloat))
+      throw Refused{PyExc_TypeError, std::string("cache: not of the attention's type, got ") + c10::toString(t.scalar_type())};
+  }
+}
+
+// (address of the lora_seqs, rows, q_start, kv_len or None, block_table or None, most rows, most sequences, plan): fills the struct
+int prepare_seqs(PyObject *const *a) {
+  Call call;
+  lora_seqs *s = seqs_at(a[0]);
+  const int32_t T = int32(a[1], "num_tokens"), most_t = int32(a[5], "max_tokens"), most_s = int32(a[6], "max_seqs");
+  const at::Tensor &qs = tensor(a[2], "q_start");
+  const int64_t S = qs.numel() - 1;
+  if (S < 0 || S > most_s)
+    throw Refused{PyExc_ValueError, "q_start: expected one more element than up to " + std::to_string(most_s) + " sequences, got " + describe(qs)};
+  if (T < 0 || T > most_t)
+    throw Refused{PyExc_ValueError, "num_tokens " + std::to_string(T) + " outside [0, " + std::to_string(most_t) + "]"};
+  const int32_t *start = vec<int32_t>(call, a[2], S + 1, "q_start"), *len = vec<int32_t>(call, a[3], S, "kv_len");
+  const int32_t *table = nullptr;
+  int64_t ld = 0;
+  if (a[4] != Py_None) {
+    if (s->page_size == 0) throw Refused{PyExc_ValueError, "block_table: these sequences have no pages"};
+    ld = table_of(call, a[4], S, s->max_pages);
+    table = static_cast<const int32_t *>(tensor(a[4], "block_table").data_ptr());
+  }
+  call.uses(tensor(a[7], "the plan"), "the plan");
+  call.stream(Py_None);  // every tensor is on the current device
+  s->q_start = start;
+  s->kv_len = len;
+  s->num_seqs = (int32_t)S;
+  s->num_tokens = T;
+  s->block_table = table;
+  s->ld_table = ld;
+  return LORA_OK;
+}
+
+// (address of the lora_seqs, of the lora_kv_cache, k, v, the cache's k and v, block_table or None, plan, stream)
+int kv_write(PyObject *const *a) {
+  Call call;
+  const lora_seqs *s = seqs_at(a[0]);
+  const lora_kv_cache *c = (const lora_kv_cache *)(intptr_t)integer(a[1]);
+  if (a[6] == Py_None) throw Refused{PyExc_ValueError, "kv_write: prepare() was given no block_table"};
+  const Mat k = rows_for(call, s, a[2], s->num_kv_heads, "k"), v = rows_for(call, s, a[3], s->num_kv_heads, "v");
+  check_cache(call, s, a[4], a[5]);
+  call.uses(tensor(a[6], "block_table"), "block_table");
+  call.uses(tensor(a[7], "the plan"), "the plan");
+  lora_stream_t st = call.stream(a[8]);
+  return unlocked([&] { return lora_kv_write(s, c, k.p, k.ld, v.p, v.ld, st); });
+}
+
+// (address of the lora_seqs, q, k, v, out, lse or None, ws, plan, stream)
+int attn_prompt(PyObject *const *a) {
+  Call call;
+  const lora_seqs *s = seqs_at(a[0]);
+  if (s->kv_len != nullptr) throw Refused{PyExc_ValueError, "attn_prompt: prepare() was given kv_len"};
+  const Mat q = rows_for(call, s, a[1], s->num_heads, "q"), k = rows_for(call, s, a[2], s->num_kv_heads, "k"),
+            v = rows_for(call, s, a[3], s->num_kv_heads, "v"), out = rows_for(call, s, a[4], s->num_heads, "out");
+  float *lse = vec<float>(call, a[5], (int64_t)s->num_tokens * s->num_heads, "lse");
+  const Scratch ws(call, a[6]);
+  call.uses(tensor(a[7], "the plan"), "the plan");
+  lora_stream_t st = call.stream(a[8]);
+  return unlocked([&] {
+    return lora_attn_prompt(s, q.p, q.ld, k.p, k.ld, v.p, v.ld, out.p, out.ld, lse, ws.p, ws.bytes, st);
+  });
+}
+
+// (address of the lora_seqs, of the lora_kv_cache, q, out, lse or None, ws, the cache's k and v, block_table or None, plan, stream)
+int attn_paged(PyObject *const *a) {
+  Call call;
+  const lora_seqs *s = seqs_at(a[0]);
+  const lora_kv_cache *c = (const lora_kv_cache *)(intptr_t)integer(a[1]);
+  if (a[8] == Py_None) throw Refused{PyExc_ValueError, "attn_paged: prepare() was given no block_table"};
+  const Mat q = rows_for(call, s, a[2], s->num_heads, "q"), out = rows_for(call, s, a[3], s->num_heads, "out");
+  float *lse = vec<float>(call, a[4], (int64_t)s->num_tokens * s->num_heads, "lse");
+  const Scratch ws(call, a[5]);
+  check_cache(call, s, a[6], a[7]);
+  call.uses(tensor(a[8], "block_table"), "block_table");
+  call.uses(tensor(a[9], "the plan"), "the plan");
+  lora_stream_t st = call.stream(a[10]);
+  return unlocked([&] { return lora_attn_paged(s, c, q.p, q.ld, out.p, out.ld, lse, ws.p, ws.bytes, st); });
+}
+
 // The Python entry of F, which takes N arguments: no C++ exception leaves it.
 template <int (*F)(PyObject *const *), int N> PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
   if (n != N) return PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", N, n);
@@ -293,6 +413,10 @@ PyMethodDef methods[] = {method<moe_route, 11>("moe_route"),
                          method<moe_act, 4>("moe_act"),
                          method<moe_act_mx4, 5>("moe_act_mx4"),
                          method<moe_combine, 6>("moe_combine"),
+                         method<prepare_seqs, 8>("prepare_seqs"),
+                         method<kv_write, 9>("kv_write"),
+                         method<attn_prompt, 9>("attn_prompt"),
+                         method<attn_paged, 11>("attn_paged"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

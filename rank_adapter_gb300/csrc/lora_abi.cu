@@ -33,11 +33,9 @@ cudaError_t set_max_dynamic_smem(const void *kernel, int bytes) {
   return e;
 }
 
-}  // namespace ra
-
 namespace {
-
 thread_local int g_last_cuda_error = 0;
+}  // namespace
 
 // Clear a launch error left in this library's runtime state by an earlier
 // failed call, so that it is not reported against the next one.
@@ -48,6 +46,13 @@ int cuda_status(cudaError_t e) {
   g_last_cuda_error = (int)e;
   return LORA_ECUDA;
 }
+
+}  // namespace ra
+
+namespace {
+
+using ra::clear_stale_error;
+using ra::cuda_status;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -184,11 +189,12 @@ const char *lora_strerror(int status) {
     case LORA_EBADSLOT: return "some token slot ids were outside [0, num_slots) and were treated as slot 0";
     case LORA_EDEVICE: return "a kernel stopped waiting on its own pipeline; the outputs since the last lora_prepare_meta are invalid";
     case LORA_EBADTOKEN: return "some token ids were outside the embedding vocabulary; their rows got no delta";
+    case LORA_EBADSEQ: return "some sequences' rows, lengths or page ids were out of range (see lora_query_seqs)";
     default: return "unknown lora_status";
   }
 }
 
-int lora_last_cuda_error(void) { return g_last_cuda_error; }
+int lora_last_cuda_error(void) { return ra::g_last_cuda_error; }
 
 uint64_t lora_launch_count(void) { return ra::g_launches.load(std::memory_order_relaxed); }
 
