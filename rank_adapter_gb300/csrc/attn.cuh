@@ -97,6 +97,8 @@ bool attn_may_split(const AttnShape &s, int64_t max_kv);
 cudaError_t launch_prepare_seqs(const lora_seqs &q, cudaStream_t st);
 cudaError_t launch_kv_write(const lora_seqs &q, const lora_kv_cache &c, const void *k, int64_t ldk, const void *v,
                             int64_t ldv, cudaStream_t st);
+bool attn_tc_takes(const AttnShape &s);
+cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t st);       // tensor cores (attn_tc.cu)
 cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t st);     // CUDA cores (attn_rows.cu)
 cudaError_t launch_attn_combine(const AttnArgs &a, cudaStream_t st);  // joins the partial results
 

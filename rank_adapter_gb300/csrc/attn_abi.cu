@@ -92,7 +92,7 @@ int run(const lora_seqs *s, ra::AttnArgs &a, const void *q, int64_t ldq, void *o
   a.ws = static_cast<float *>(ws);
   a.num_tokens = s->num_tokens;
   const int64_t max_kv = has_cache(s) ? (int64_t)s->page_size * s->max_pages : s->num_tokens;
-  cudaError_t e = ra::launch_attn_rows(a, (cudaStream_t)stream);
+  cudaError_t e = a.s.tc ? ra::launch_attn_tc(a, (cudaStream_t)stream) : ra::launch_attn_rows(a, (cudaStream_t)stream);
   if (e == cudaSuccess && ra::attn_may_split(a.s, max_kv)) e = ra::launch_attn_combine(a, (cudaStream_t)stream);
   return cuda_status(e);
 }

@@ -23,11 +23,11 @@ AttnShape attn_shape(const lora_seqs &q) {
   s.G = s.Hq / s.Hkv;
   s.D = q.head_dim;
   s.causal = q.causal != 0;
-  s.tc = false;
-  s.tile_tokens = std::max(1, 32 / s.G);
-  s.unit_tokens = s.tile_tokens;
-  s.slot_rows = std::max(32, s.G);
-  s.ctas = 2 * std::max(1, sm_count());
+  s.tc = attn_tc_takes(s);
+  s.tile_tokens = s.tc ? 128 / s.G : std::max(1, 32 / s.G);
+  s.unit_tokens = s.tc ? 2 * s.tile_tokens : s.tile_tokens;
+  s.slot_rows = s.tc ? 256 : std::max(32, s.G);
+  s.ctas = (s.tc ? 1 : 2) * std::max(1, sm_count());
   s.min_cost = 2;
   s.max_slots = 2 * s.ctas / s.Hkv + 2;
   s.scale_log2 = (float)((double)q.scale * 1.4426950408889634);

@@ -1,0 +1,678 @@
+// Attention on the tensor cores (bf16, heads of 64 and 128).
+//
+// Rows of a tile are 128 (token, query head) pairs of one key-value head, so that a
+// group of heads shares each key and value that is loaded; a CTA works on two streams
+// of (tile, 128 keys) steps at once, one softmax warpgroup each, so that the tensor
+// core multiplies for one stream while the other takes its exponentials:
+//   S = Q K^T    both operands in shared memory, S in TMEM (fp32)
+//   P = 2^(c S - m)    a thread a row, S from TMEM, P back over S as bf16
+//   O += P V     P from TMEM, V from shared memory as it lies there
+// A unit of two tiles gives a stream to each; a unit of one tile alternates its key
+// blocks between the streams and adds up both results. Streams alternate strictly, over
+// units' ends as well, and the score product of a stream's next step is issued right
+// behind the product that reads its P.
+//
+// The running maximum of a row rises only when a block exceeds it by more than 2^8 (all
+// weights carry the same factor, fp32 and bf16 have the range for it), so that O is
+// rescaled in few steps. S of a step is complete only once every MMA issued before it
+// is, the stream's last product with V among them: O can be rescaled without a wait.
+//
+// Values that some row of a unit does not see (behind the keys, of later tokens) are
+// looked at by a warp of its own before the MMA, since 0 * NaN is NaN: rows behind
+// the keys are zeroed, and where a later token's value is not finite it is taken out and
+// added to the rows that see it at the end.
+#include "attn.cuh"
+#include "tcgen05.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kRows = 128;      // rows of a tile
+constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kFixWarp = 11;
+constexpr int kThreads = 32 * 12;
+constexpr float kLazy = 8.f;    // log2 of the factor that a weight may exceed 1 by
+constexpr int kFlags = 8;       // units that the loads can be ahead of an epilogue, and more
+
+template <int D_>
+struct TcShape {
+  static constexpr int D = D_, kHalves = D / 64;
+  static constexpr int kHalfBytes = kRows * 128;              // 128 rows of 64 elements
+  static constexpr int kTileBytes = kHalves * kHalfBytes;     // Q tile, K or V block
+  static constexpr int kK = D == 128 ? 3 : 5, kV = D == 128 ? 2 : 5;  // K and V blocks in flight
+  static constexpr int kKOff = 2 * kTileBytes, kVOff = kKOff + kK * kTileBytes;
+  static constexpr int kStatOff = kVOff + kV * kTileBytes;    // {m, l} of a merged stream's rows
+  static constexpr int kBarOff = kStatOff + kRows * 8;
+  static constexpr int kBarriers = 2 * kK + 3 * kV + 13;
+  static constexpr int kSmem = 1024 + kBarOff + kBarriers * 8 + 16 + kFlags * 4;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  // TMEM columns: two streams' S (and P over it), two streams' O.
+  static constexpr uint32_t kS = 0, kO = 256, kTmemCols = 512;
+};
+
+struct TcMaps {
+  CUtensorMap q;     // {D, heads, rows}, boxes of 64 x group x tile tokens
+  CUtensorMap k, v;  // packed rows: {D, heads, rows}, boxes of 64 x 1 x 128; pages: {D, keys of a page, heads, pages}, 64 x keys x 1 x 1
+};
+
+// ------------------------------------------------------------------ PTX
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+// Four MMAs of 16 keys each: A (P) in TMEM, 8 columns a step, B (V) in shared memory. Every lane of the warp calls it.
+__device__ __forceinline__ void mma_pv4(uint32_t d, uint32_t p, uint64_t bd, uint64_t b_step, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred q, e, t;\n\t.reg .b32 r, a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+      "elect.sync r|e, 0xffffffff;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 t, %3, %3;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+      "add.s64 b1, %2, %5;\n\tadd.s64 b2, b1, %5;\n\tadd.s64 b3, b2, %5;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}"
+      ::"r"(d), "r"(p), "l"(bd), "r"(idesc), "r"(acc), "l"(b_step) : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
+        "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// kind::f16 with fp32 accumulator and both operands K-major.
+__host__ __device__ constexpr uint32_t idesc_kk(int M, int N) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// ------------------------------------------------------------------ walk over a CTA's items
+
+// Item k of this CTA (a unit of one key-value head): the units lie in order of falling cost; every other round of
+// CTAs runs backwards.
+struct Item {
+  AttnUnit u;
+  int head, blocks, steps;
+  bool pair;
+};
+
+struct Walk {
+  const AttnArgs &a;
+  int64_t n, k = 0;
+  uint32_t g = 0;        // steps before the current item: stream of step i is (g + i) & 1
+  uint32_t index = 0;    // items before it
+  int4 r0, r1;           // the next item's record
+  int64_t at = 0;
+  __device__ __forceinline__ explicit Walk(const AttnArgs &args)
+      : a(args), n((int64_t)args.plan[AttnPlan::kUnits] * args.s.Hkv) { fetch(); }
+  __device__ __forceinline__ void fetch() {
+    const int64_t c = (k & 1) ? (int64_t)gridDim.x - 1 - blockIdx.x : (int64_t)blockIdx.x;
+    at = k * gridDim.x + c;
+    if (at < n) {
+      const int4 *p = reinterpret_cast<const int4 *>(a.plan + a.p.units() + AttnPlan::kUnit * (at / a.s.Hkv));
+      r0 = p[0];
+      r1 = p[1];
+    }
+  }
+  // False at the end. Call done() after each item.
+  __device__ __forceinline__ bool item(Item &it) {
+    if (at >= n) return false;
+    it.u = AttnUnit{r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+    it.head = (int)(at % a.s.Hkv);
+    it.blocks = it.u.kb1 - it.u.kb0;
+    it.pair = it.u.tokens > a.s.tile_tokens;
+    it.steps = it.pair ? 2 * it.blocks : it.blocks;
+    ++k;
+    fetch();
+    return true;
+  }
+  __device__ __forceinline__ void done(const Item &it) {
+    g += it.steps;
+    ++index;
+  }
+  // The first step of stream t in the item, and how many it has.
+  __device__ __forceinline__ int first(int t) const { return (int)((g ^ (uint32_t)t) & 1u); }
+  __device__ __forceinline__ int count(const Item &it, int t) const {
+    const int i = first(t);
+    return i < it.steps ? (it.steps - i + 1) / 2 : 0;
+  }
+};
+
+// Keys that every row of a unit sees.
+__device__ __forceinline__ int common_keys(const AttnUnit &u, int causal) { return visible_keys(u.pos0, u.kv_len, causal); }
+
+// ------------------------------------------------------------------ kernel
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ TcMaps maps, const AttnArgs a) {
+  using S = TcShape<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *sm = align1024(smem_raw);
+  uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + S::kBarOff);  // a K block is in
+  uint64_t *kfree = kfull + S::kK;       // its MMAs are done
+  uint64_t *vfull = kfree + S::kK;       // a V block is in
+  uint64_t *vfree = vfull + S::kV;       // its MMAs are done
+  uint64_t *fixed = vfree + S::kV;       // it has been looked at
+  uint64_t *qfull = fixed + S::kV;       // a stream's Q tile is in
+  uint64_t *qfree = qfull + 2;           // its last score product is done
+  uint64_t *sfull = qfree + 2;           // S of a stream's step is in TMEM
+  uint64_t *pfull = sfull + 2;           // P of it is
+  uint64_t *ofull = pfull + 2;           // a stream's last product with V is done
+  uint64_t *mfull = ofull + 2;           // the statistics of the stream to merge are in shared memory
+  uint64_t *mfree = mfull + 1;           // its O has been read
+  uint64_t *fin = mfree + 1;
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(fin + 1);
+  volatile int32_t *flags = reinterpret_cast<int32_t *>(tslot + 1);  // [item % kFlags]: the last item with values taken out
+  float2 *stats = reinterpret_cast<float2 *>(sm + S::kStatOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kK; ++i) {
+      mbar_init(&kfull[i], 1);
+      mbar_init(&kfree[i], 1);
+    }
+    for (int i = 0; i < S::kV; ++i) {
+      mbar_init(&vfull[i], 1);
+      mbar_init(&vfree[i], 1);
+      mbar_init(&fixed[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&qfull[t], 1);
+      mbar_init(&qfree[t], 1);
+      mbar_init(&sfull[t], 1);
+      mbar_init(&pfull[t], 4);
+      mbar_init(&ofull[t], 1);
+    }
+    mbar_init(mfull, 4);
+    mbar_init(mfree, 4);
+    mbar_init(fin, 1);
+    for (int i = 0; i < kFlags; ++i) flags[i] = -1;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(tslot, S::kTmemCols);
+  if (warp == kKWarp && lane < 2) prefetch_map(lane == 0 ? &maps.k : &maps.q);
+  if (warp == kVWarp && lane == 0) prefetch_map(&maps.v);
+  pdl_wait();
+  tc_before_sync();
+  __syncthreads();
+  tc_after_sync();
+  pdl_trigger();  // only now: a successor that takes TMEM must not start before this CTA has its own
+  const uint32_t tmem = *tslot;
+  Walk w(a);
+  Item it;
+
+  // The softmax warps hold a row of S: registers of the others' share go to them (2 * 216 + 72 = 3 * 168).
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == kKWarp || warp == kVWarp) {
+      // ---- loads: one warp K blocks and Q tiles, one V blocks
+      const bool keys = warp == kKWarp;
+      const uint32_t n_slots = keys ? S::kK : S::kV;
+      uint64_t *full = keys ? kfull : vfull, *free = keys ? kfree : vfree;
+      const CUtensorMap *map = keys ? &maps.k : &maps.v;
+      unsigned char *ring = sm + (keys ? S::kKOff : S::kVOff);
+      const int half = lane % S::kHalves, part = lane / S::kHalves;
+      uint32_t slot = 0, phase = 0, used[2] = {0, 0};
+      bool ok = true;
+      while (ok && w.item(it)) {
+        const int64_t row0 = (int64_t)it.u.row0 - it.u.pos0;  // packed rows: the sequence's first
+        for (int b = 0; b < it.blocks; ++b) {
+          const int j0 = (it.u.kb0 + b) * kKeyBlock;
+          int page = 0, copies = S::kHalves, in_page = 0, rows = kKeyBlock;  // copies of a block, rows of each
+          if constexpr (PAGED) {
+            // A lane a page: its id, or one past the cache (which reads zeros).
+            const int ps = a.kv.page_size;
+            rows = min(ps, kKeyBlock);
+            copies = (min(kKeyBlock, it.u.kv_len - j0) + rows - 1) / rows * S::kHalves;
+            const int j = j0 + part * rows;
+            in_page = j & (ps - 1);
+            if (lane < copies) {
+              page = a.kv.table[(int64_t)it.u.seq * a.kv.ld_table + (j >> a.kv.log2_page)];
+              if ((unsigned)page >= (unsigned)a.kv.num_pages) {
+                atomicOr(a.err, kErrBadPage);
+                page = a.kv.num_pages;
+              }
+            }
+          }
+          if (!mbar_wait_warp(&free[slot], phase ^ 1, a.err, kErrAttn)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_tx(&full[slot], (uint32_t)(copies * rows * 128));
+          __syncwarp();
+          unsigned char *dst = ring + slot * S::kTileBytes + half * S::kHalfBytes;
+          if (lane < copies) {
+            if constexpr (PAGED) tma_load_4d(dst + part * rows * 128, map, half * 64, in_page, it.head, page, &full[slot]);
+            else tma_load_3d(dst, map, half * 64, it.head, (int)(row0 + j0), &full[slot]);
+          }
+          if (++slot == n_slots) {
+            slot = 0;
+            phase ^= 1;
+          }
+          if (!keys || b != min(1, it.blocks - 1)) continue;
+          // Q tiles, behind the first two K blocks, which need not wait for the previous unit's last scores: a
+          // stream's own where there are two, the same for both where there is one.
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (!ok || w.count(it, t) == 0) continue;
+            if (!mbar_wait_warp(&qfree[t], (used[t] & 1) ^ 1, a.err, kErrAttn)) { ok = false; continue; }
+            ++used[t];
+            if (lane == 0) mbar_arrive_tx(&qfull[t], (uint32_t)(S::kHalves * a.s.tile_tokens * a.s.G * 128));
+            __syncwarp();
+            if (lane < S::kHalves)
+              tma_load_3d(sm + t * S::kTileBytes + lane * S::kHalfBytes, &maps.q, lane * 64, it.head * a.s.G,
+                          it.u.row0 + (it.pair ? w.first(t) * a.s.tile_tokens : 0), &qfull[t]);
+          }
+          if (!ok) break;
+        }
+        w.done(it);
+      }
+    } else if (warp == kFixWarp) {
+      // ---- values that not every row sees
+      uint32_t slot = 0, phase = 0;
+      bool ok = true;
+      while (ok && w.item(it)) {
+        const int seen = common_keys(it.u, a.s.causal);
+        for (int b = 0; b < it.blocks && ok; ++b) {
+          const uint32_t v = slot;
+          const int j0 = (it.u.kb0 + b) * kKeyBlock;
+          if (!mbar_wait_warp(&vfull[v], phase, a.err, kErrAttn)) { ok = false; break; }
+          if (++slot == S::kV) {
+            slot = 0;
+            phase ^= 1;
+          }
+          if (j0 + kKeyBlock <= seen) {
+            if (lane == 0) mbar_arrive(&fixed[v]);
+            continue;
+          }
+          unsigned char *base = sm + S::kVOff + v * S::kTileBytes;
+          const int r0 = max(0, seen - j0), r1 = min(kKeyBlock, it.u.kv_len - j0);  // looked at; zeroed from r1 on
+          bool any = false;
+          for (int i = lane; i < (r1 - r0) * (D / 8); i += 32) {
+            const int r = r0 + i / (D / 8), c = i % (D / 8);
+            uint4 *p = reinterpret_cast<uint4 *>(base + (c / 8) * S::kHalfBytes + swz128(r, c % 8));
+            const uint4 x = *p;
+            uint32_t q[4] = {x.x, x.y, x.z, x.w};
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // exponents of all ones
+              if ((q[e] & 0x7f80u) == 0x7f80u) { q[e] &= 0xffff0000u; bad = true; }
+              if ((q[e] & 0x7f800000u) == 0x7f800000u) { q[e] &= 0xffffu; bad = true; }
+            }
+            if (bad) {
+              *p = make_uint4(q[0], q[1], q[2], q[3]);
+              any = true;
+            }
+          }
+          for (int i = lane; i < (kKeyBlock - r1) * (D / 8); i += 32) {
+            const int r = r1 + i / (D / 8), c = i % (D / 8);
+            *reinterpret_cast<uint4 *>(base + (c / 8) * S::kHalfBytes + swz128(r, c % 8)) = make_uint4(0, 0, 0, 0);
+          }
+          if (any) flags[w.index % kFlags] = (int)w.index;
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&fixed[v]);
+        }
+        w.done(it);
+      }
+    } else {
+      // ---- MMA issue. The score products run two steps ahead of the others, over units' ends as well.
+      constexpr uint32_t id_s = idesc_kk(kRows, kKeyBlock), id_o = idesc_bf16(kRows, D);
+      Walk ws(a);  // of the score products
+      Item is{};
+      int si = 0;  // their next step in it
+      bool more = ws.item(is), ok = true;
+      uint32_t sslot = 0, sphase = 0;    // slot of its K block
+      uint32_t qused[2] = {0, 0}, pused[2] = {0, 0};
+      uint32_t slot = 0, phase = 0;      // slot of the other products' V block
+      auto scores = [&]() -> bool {  // the next step's scores
+        while (more && si == is.steps) {
+          ws.done(is);
+          more = ws.item(is);
+          si = 0;
+        }
+        if (!more) return true;
+        const int t = (int)((ws.g + si) & 1u);
+        if (si < 2) {
+          if (!mbar_wait_warp(&qfull[t], qused[t] & 1, a.err, kErrAttn)) return false;
+          ++qused[t];
+        }
+        if (!is.pair || (si & 1) == 0)
+          if (!mbar_wait_warp(&kfull[sslot], sphase, a.err, kErrAttn)) return false;
+        tc_after_sync();
+        const uint32_t q = smem_addr(sm + t * S::kTileBytes), k = smem_addr(sm + S::kKOff + sslot * S::kTileBytes);
+#pragma unroll
+        for (int h = 0; h < S::kHalves; ++h)
+          mma_run<4>(tmem + S::kS + t * 128, smem_desc(q + h * S::kHalfBytes, 16, 1024, kSw128),
+                     smem_desc(k + h * S::kHalfBytes, 16, 1024, kSw128), 2, 2, id_s, h > 0);
+        mma_commit_elect(&sfull[t]);
+        if (si + 2 >= is.steps) mma_commit_elect(&qfree[t]);
+        if (!is.pair || (si & 1) == 1) {
+          mma_commit_elect(&kfree[sslot]);
+          if (++sslot == S::kK) {
+            sslot = 0;
+            sphase ^= 1;
+          }
+        }
+        ++si;
+        return true;
+      };
+      ok = scores() && scores();
+      while (ok && w.item(it)) {
+        for (int i = 0; i < it.steps && ok; ++i) {
+          const int t = (int)((w.g + i) & 1u);
+          if (!it.pair || (i & 1) == 0)
+            if (!mbar_wait_warp(&fixed[slot], phase, a.err, kErrAttn)) { ok = false; break; }
+          if (!mbar_wait_warp(&pfull[t], pused[t] & 1, a.err, kErrAttn)) { ok = false; break; }
+          ++pused[t];
+          tc_after_sync();
+          const uint32_t vs = smem_addr(sm + S::kVOff + slot * S::kTileBytes);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)  // 64 keys each
+            mma_pv4(tmem + S::kO + t * 128, tmem + S::kS + t * 128 + h * 32,
+                    smem_desc(vs + h * 64 * 128, S::kHalfBytes, 1024, kSw128), 128, id_o, i >= 2 || h > 0);
+          if (i + 2 >= it.steps) mma_commit_elect(&ofull[t]);
+          if (!it.pair || (i & 1) == 1) {
+            mma_commit_elect(&vfree[slot]);
+            if (++slot == S::kV) {
+              slot = 0;
+              phase ^= 1;
+            }
+          }
+          ok = scores();
+        }
+        w.done(it);
+      }
+      mma_commit_elect(fin);
+      mbar_wait_warp(fin, 0, a.err, kErrAttn);  // every MMA is done before TMEM is freed
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // ---- softmax of stream t, a thread a row
+    const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t ts = tmem + lanes + S::kS + t * 128, to = tmem + lanes + S::kO;
+    const float c = a.s.scale_log2;
+    uint32_t sused = 0, oused[2] = {0, 0}, merges = 0;
+    bool ok = true;
+    while (ok && w.item(it)) {
+      const int i0 = w.first(t), mine = w.count(it, t), other = w.count(it, t ^ 1);
+      const bool writes = it.pair || i0 == 0;  // the stream whose warpgroup stores the rows
+      // The row: its token and head, and the keys it sees.
+      const int tile = it.pair ? i0 : 0, tok = tile * a.s.tile_tokens + r / a.s.G;
+      const bool live = r < a.s.tile_tokens * a.s.G && tok < it.u.tokens;
+      const bool busy = __any_sync(0xffffffffu, live);
+      const int lim = live ? visible_keys(it.u.pos0 + tok, it.u.kv_len, a.s.causal) : INT32_MAX / 2;
+      float m = -INFINITY, l = 0.f;  // of c * s
+      for (int n = 0; n < mine && ok; ++n) {
+        const int i = i0 + 2 * n, j0 = (it.u.kb0 + (it.pair ? i >> 1 : i)) * kKeyBlock;
+        if (!mbar_wait_warp(&sfull[t], sused & 1, a.err, kErrAttn)) { ok = false; break; }
+        ++sused;
+        if (busy) {
+          tc_after_sync();
+          float s[128];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) tmem_ld32_async(ts + 32 * x, s + 32 * x);
+          tmem_wait_ld();
+          const int sees = lim - j0;
+          if (__any_sync(0xffffffffu, sees < kKeyBlock)) {
+#pragma unroll
+            for (int x = 0; x < 128; ++x) s[x] = x < sees ? s[x] : -INFINITY;
+          }
+          float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int x = 4; x < 128; ++x) top[x & 3] = fmaxf(top[x & 3], s[x]);
+          const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+          const bool rise = mn > m + kLazy;
+          if (__any_sync(0xffffffffu, rise)) {
+            const float up = rise ? ex2(m - mn) : 1.f;
+            if (rise) m = mn;
+            l *= up;
+            if (n > 0) {
+#pragma unroll 1
+              for (int x = 0; x < D; x += 16) {
+                float o[16];
+                tmem_ld16(to + t * 128 + x, o);
+#pragma unroll
+                for (int y = 0; y < 16; ++y) o[y] *= up;
+                tmem_st16(to + t * 128 + x, o);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+          const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t p[32];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              float2 e = fma2(make_float2(s[64 * h + 2 * x], s[64 * h + 2 * x + 1]), c2, b2);
+              e.x = ex2(e.x);
+              e.y = ex2(e.y);
+              sum[x & 1] = add2(sum[x & 1], e);
+              p[x] = pack_bf16(e.x, e.y);
+            }
+            tmem_st32(ts + 32 * h, p);
+          }
+          sum[0] = add2(sum[0], sum[1]);
+          l += sum[0].x + sum[0].y;
+          tmem_wait_st();
+          tc_before_sync();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[t]);
+      }
+      if (!ok) break;
+      // ---- the end of the unit
+      const bool merge = !it.pair && other > 0 && mine > 0;
+      if (!writes) {
+        oused[t] += mine > 0;
+        oused[t ^ 1] += other > 0;
+        if (merge) {
+          stats[r] = make_float2(m, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(mfull);
+          if (!mbar_wait_warp(mfree, merges & 1, a.err, kErrAttn)) { ok = false; break; }
+          ++merges;
+        }
+        w.done(it);
+        continue;
+      }
+      float w0 = 1.f, w1 = 0.f;  // weights of this stream's and the other's O
+      if (mine > 0) {
+        if (!mbar_wait_warp(&ofull[t], oused[t] & 1, a.err, kErrAttn)) { ok = false; break; }
+        ++oused[t];
+      }
+      if (merge) {
+        if (!mbar_wait_warp(&ofull[t ^ 1], oused[t ^ 1] & 1, a.err, kErrAttn) ||
+            !mbar_wait_warp(mfull, merges & 1, a.err, kErrAttn)) { ok = false; break; }
+        ++merges;
+        const float2 o = stats[r];
+        const float mm = fmaxf(m, o.x), base = mm == -INFINITY ? 0.f : mm;
+        w0 = ex2(m - base);
+        w1 = ex2(o.x - base);
+        l = l * w0 + o.y * w1;
+        m = mm;
+      }
+      oused[t ^ 1] += other > 0;
+      tc_after_sync();
+      const int64_t row = (int64_t)it.u.row0 + tok;
+      const int head = it.head * a.s.G + r % a.s.G;
+      const bool split = it.u.slot >= 0, some = it.steps > 0;
+      const float inv = split ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      w0 *= inv;
+      w1 *= inv;
+      const bool taken = some && flags[w.index % kFlags] == (int)w.index;
+      if (busy) {
+        float *part = nullptr;
+        if (split) part = a.ws + ((int64_t)it.u.slot * a.s.Hkv + it.head) * slot_floats(a.s);
+        const int unit_row = tile * a.s.tile_tokens * a.s.G + r;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + row * a.ldo + (int64_t)head * D;
+#pragma unroll 1
+        for (int x = 0; x < D; x += 32) {
+          float o[32];
+          if (some) {
+            tmem_ld32_async(to + t * 128 + x, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = some ? o[y] * w0 : 0.f;
+          if (merge) {
+            float o1[32];
+            tmem_ld32_async(to + (t ^ 1) * 128 + x, o1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = fmaf(o1[y], w1, o[y]);
+          }
+          if (taken && live) {
+            // Values that were taken out, for the rows that see them.
+            const int end = min(lim, it.u.kb1 * kKeyBlock);
+            for (int j = max(common_keys(it.u, a.s.causal), it.u.kb0 * kKeyBlock); j < end; ++j) {
+              int64_t at = -1;
+              if constexpr (PAGED) {
+                const int page = a.kv.table[(int64_t)it.u.seq * a.kv.ld_table + (j >> a.kv.log2_page)];
+                if ((unsigned)page < (unsigned)a.kv.num_pages) at = page * a.kv.v_page + (j & (a.kv.page_size - 1)) * a.kv.v_row;
+              } else {
+                at = ((int64_t)it.u.row0 - it.u.pos0 + j) * a.kv.v_row;
+              }
+              if (at < 0) continue;
+              const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.kv.v) + at + it.head * a.kv.v_head + x;
+#pragma unroll
+              for (int y = 0; y < 32; ++y) {
+                const float f = __bfloat162float(v[y]);
+                if (!isfinite(f)) o[y] += f;
+              }
+            }
+          }
+          if (live) {
+            if (split) {
+              float4 *d = reinterpret_cast<float4 *>(part + (int64_t)unit_row * D + x);
+#pragma unroll
+              for (int y = 0; y < 8; ++y) d[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+            } else {
+              uint4 *d = reinterpret_cast<uint4 *>(out + x);
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                d[y] = make_uint4(pack_bf16(o[8 * y], o[8 * y + 1]), pack_bf16(o[8 * y + 2], o[8 * y + 3]),
+                                  pack_bf16(o[8 * y + 4], o[8 * y + 5]), pack_bf16(o[8 * y + 6], o[8 * y + 7]));
+            }
+          }
+        }
+        if (live) {
+          if (split) *reinterpret_cast<float2 *>(part + (int64_t)a.s.slot_rows * D + 2 * unit_row) = make_float2(m, l);
+          else if (a.lse != nullptr) a.lse[row * a.s.Hq + head] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+        }
+      }
+      tc_before_sync();
+      if (merge) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(mfree);
+      }
+      w.done(it);
+    }
+  }
+  tc_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_after_sync();
+    tmem_free(tmem, S::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+cudaError_t encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                   const cuuint32_t *box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, es,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Rows of `heads` heads of D elements, boxes of 64 elements x box_heads x box_rows.
+cudaError_t encode_rows(CUtensorMap *m, const void *base, int D, int heads, int64_t head, int64_t rows, int64_t ld, int box_heads,
+                        int box_rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)head * 2, (cuuint64_t)ld * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  return encode(m, base, 3, dims, strides, box);
+}
+
+cudaError_t encode_pages(CUtensorMap *m, const void *base, const AttnArgs &a, int64_t row, int64_t head, int64_t page) {
+  const cuuint64_t dims[4] = {(cuuint64_t)a.s.D, (cuuint64_t)a.kv.page_size, (cuuint64_t)a.s.Hkv, (cuuint64_t)a.kv.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)row * 2, (cuuint64_t)head * 2, (cuuint64_t)page * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)std::min(a.kv.page_size, kKeyBlock), 1, 1};
+  return encode(m, base, 4, dims, strides, box);
+}
+
+template <int D, bool PAGED>
+cudaError_t launch(const AttnArgs &a, cudaStream_t st) {
+  TcMaps maps;
+  cudaError_t e = encode_rows(&maps.q, a.q, D, a.s.Hq, D, a.num_tokens, a.ldq, a.s.G, a.s.tile_tokens);
+  if (PAGED) {
+    if (e == cudaSuccess) e = encode_pages(&maps.k, a.kv.k, a, a.kv.k_row, a.kv.k_head, a.kv.k_page);
+    if (e == cudaSuccess) e = encode_pages(&maps.v, a.kv.v, a, a.kv.v_row, a.kv.v_head, a.kv.v_page);
+  } else {
+    if (e == cudaSuccess) e = encode_rows(&maps.k, a.kv.k, D, a.s.Hkv, a.kv.k_head, a.num_tokens, a.kv.k_row, 1, kKeyBlock);
+    if (e == cudaSuccess) e = encode_rows(&maps.v, a.kv.v, D, a.s.Hkv, a.kv.v_head, a.num_tokens, a.kv.v_row, 1, kKeyBlock);
+  }
+  if (e == cudaSuccess) e = set_max_dynamic_smem((const void *)attn_tc_kernel<D, PAGED>, TcShape<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t most = (int64_t)a.p.max_units * a.s.Hkv;
+  return launch_pdl(attn_tc_kernel<D, PAGED>, dim3((unsigned)std::min<int64_t>(most, a.s.ctas)), dim3(kThreads), TcShape<D>::kSmem,
+                    st, 1u, maps, a);
+}
+
+}  // namespace
+
+bool attn_tc_takes(const AttnShape &s) {
+  return s.dtype == LORA_BF16 && (s.D == 64 || s.D == 128) && s.G <= kRows && sgmv_supported();
+}
+
+cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t st) {
+  const bool paged = a.kv.page_size > 0;
+  if (a.s.D == 128) return paged ? launch<128, true>(a, st) : launch<128, false>(a, st);
+  return paged ? launch<64, true>(a, st) : launch<64, false>(a, st);
+}
+
+}  // namespace ra

@@ -86,6 +86,19 @@ def test_split_keys(lib, heads, new, before):
         assert torch.equal(first, s.out)
 
 
+@pytest.mark.parametrize("heads", [(8, 8, 128), (8, 8, 64), (16, 4, 128)], ids=str)
+def test_long_units(lib, heads):
+    """So many sequences that none is split: a CTA walks several units of up to a dozen blocks of keys, odd and even, one and two tiles."""
+    r = np.random.default_rng(14)
+    s = Step(*heads, [1] * 20 + [2, 3, 40, 1, 100, 1] * 2, [int(x) for x in r.integers(1, 1500, 32)], seed=14)
+    s.write()
+    s.paged()
+    s.check()
+    s = Step(heads[0], heads[1], heads[2], [700, 1, 333, 20], seed=15)
+    s.prompt()
+    s.check()
+
+
 @pytest.mark.parametrize("dtype,heads", [(BF16, (4, 2, 64)), (BF16, (2, 2, 128)), (F32, (4, 2, 64))])
 def test_rows_without_keys(lib, dtype, heads):
     """Fewer keys than rows: the first rows see nothing under a causal mask, and get zeros and -inf."""
