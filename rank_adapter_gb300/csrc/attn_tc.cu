@@ -1,24 +1,27 @@
 // Attention on the tensor cores (bf16, heads of 64 and 128).
 //
 // Rows of a tile are 128 (token, query head) pairs of one key-value head, so that a
-// group of heads shares each key and value that is loaded; a CTA works on two streams
-// of (tile, 128 keys) steps at once, one softmax warpgroup each, so that the tensor
-// core multiplies for one stream while the other takes its exponentials:
+// group of heads shares each key and value that is loaded. A CTA works on two streams of
+// (tile, 128 keys) steps at once, each with a softmax warpgroup and a warp that issues its
+// MMAs, so that the tensor core multiplies for one stream while the other takes its
+// exponentials:
 //   S = Q K^T    both operands in shared memory, S in TMEM (fp32)
 //   P = 2^(c S - m)    a thread a row, S from TMEM, P back over S as bf16
-//   O += P V     P from TMEM, V from shared memory as it lies there
-// A unit of two tiles gives a stream to each; a unit of one tile alternates its key
-// blocks between the streams and adds up both results. Streams alternate strictly, over
-// units' ends as well, and the score product of a stream's next step is issued right
-// behind the product that reads its P.
+//   O += P V     P from TMEM, V from shared memory as it lies there; in two halves of the
+//                keys, the first while the second's exponentials are taken
+// A unit of two tiles gives one to each stream; a unit of one tile deals its blocks of keys
+// out to both, and their results are added up. A stream's next scores are issued right
+// behind the product that reads its P (MMAs of one thread run in order), over units' ends
+// as well. (One warp that issued both streams' MMAs spent 1750 clocks a step on them and on
+// its waits, of which the MMAs take 1024.)
 //
 // The running maximum of a row rises only when a block exceeds it by more than 2^8 (all
 // weights carry the same factor, fp32 and bf16 have the range for it), so that O is
-// rescaled in few steps. S of a step is complete only once every MMA issued before it
-// is, the stream's last product with V among them: O can be rescaled without a wait.
+// rescaled in few steps. S of a step is complete only once every MMA that its warp issued
+// before is, the last product with V among them: O can be rescaled without a wait.
 //
 // Values that some row of a unit does not see (behind the keys, of later tokens) are
-// looked at by a warp of its own before the MMA, since 0 * NaN is NaN: rows behind
+// looked at by warps of their own before the MMA, since 0 * NaN is NaN: rows behind
 // the keys are zeroed, and where a later token's value is not finite it is taken out and
 // added to the rows that see it at the end.
 #include "attn.cuh"
@@ -28,8 +31,11 @@ namespace ra {
 namespace {
 
 constexpr int kRows = 128;      // rows of a tile
-constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kFixWarp = 11;
-constexpr int kThreads = 32 * 12;
+// Warps: 0-3 and 4-7 the streams' softmax, then their MMAs, the loads, the values that not every row sees.
+constexpr int kMmaWarp = 8, kKWarp = 10, kVWarp = 11, kFixWarp = 12, kFixWarps = 4;
+constexpr int kThreads = 32 * (kFixWarp + kFixWarps);
+// Registers: the softmax warps hold a row of S. 8 * 200 + 8 * 56 = 16 * 128, the launch's own.
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 56;
 constexpr float kLazy = 8.f;    // log2 of the factor that a weight may exceed 1 by
 constexpr int kFlags = 8;       // units that the loads can be ahead of an epilogue, and more
 
@@ -38,12 +44,16 @@ struct TcShape {
   static constexpr int D = D_, kHalves = D / 64;
   static constexpr int kHalfBytes = kRows * 128;              // 128 rows of 64 elements
   static constexpr int kTileBytes = kHalves * kHalfBytes;     // Q tile, K or V block
-  static constexpr int kK = D == 128 ? 3 : 5, kV = D == 128 ? 2 : 5;  // K and V blocks in flight
-  static constexpr int kKOff = 2 * kTileBytes, kVOff = kKOff + kK * kTileBytes;
-  static constexpr int kStatOff = kVOff + kV * kTileBytes;    // {m, l} of a merged stream's rows
+  // K and V blocks in flight. Even, so that where the streams take blocks in turn each has
+  // slots of its own.
+  static constexpr uint32_t kK = D == 128 ? 2 : 4, kV = D == 128 ? 2 : 4;
+  static constexpr int kKOff = 2 * kTileBytes, kVOff = kKOff + (int)kK * kTileBytes;
+  static constexpr int kTurnOff = kVOff + (int)kV * kTileBytes;   // a softmax warp's 32 rows of 128 bytes on their way out
+  static constexpr int kTurnBytes = 32 * 128;
+  static constexpr int kStatOff = kTurnOff + 8 * kTurnBytes;  // {m, l} of a merged stream's rows
   static constexpr int kBarOff = kStatOff + kRows * 8;
-  static constexpr int kBarriers = 2 * kK + 3 * kV + 13;
-  static constexpr int kSmem = 1024 + kBarOff + kBarriers * 8 + 16 + kFlags * 4;
+  static constexpr int kBarriers = 2 * (int)kK + 3 * (int)kV + 18;
+  static constexpr int kSmem = 1024 + kBarOff + kBarriers * 8 + 16 + kFlags * 4 + 8;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   // TMEM columns: two streams' S (and P over it), two streams' O.
   static constexpr uint32_t kS = 0, kO = 256, kTmemCols = 512;
@@ -102,6 +112,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+  return m;
+}
 // Two fp32 operations an instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -126,30 +141,48 @@ __host__ __device__ constexpr uint32_t idesc_kk(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// mbar_wait_warp, but for its first look at the clock: reading %globaltimer takes longer than most of these waits.
+__device__ __forceinline__ bool await(uint64_t *b, uint32_t parity, int *err, int code) {
+  bool ok = mbar_try(b, parity);
+  for (int i = 0; !ok && i < 32; ++i) ok = mbar_try(b, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  return mbar_wait_warp(b, parity, err, code);
+}
+
+// Waits, for up to kWaitNs, until *at is past pos.
+__device__ __forceinline__ bool past(const volatile uint32_t *at, uint32_t pos, int *err, int code) {
+  const uint64_t t0 = *at > pos ? 0 : global_ns();
+  while (*at <= pos)
+    if (global_ns() - t0 > kWaitNs) {
+      atomicOr(err, code);
+      return false;
+    }
+  __threadfence_block();
+  return true;
+}
+
 // ------------------------------------------------------------------ walk over a CTA's items
 
 // Item k of this CTA (a unit of one key-value head): the units lie in order of falling cost; every other round of
 // CTAs runs backwards.
 struct Item {
   AttnUnit u;
-  int head, blocks, steps;
+  int head, blocks;
   bool pair;
 };
 
 struct Walk {
   const AttnArgs &a;
-  int64_t n, k = 0;
-  uint32_t g = 0;        // steps before the current item: stream of step i is (g + i) & 1
+  uint32_t n, at, k = 0;
+  uint32_t pos = 0;      // blocks before the current item: block b of one tile belongs to stream (pos + b) & 1
   uint32_t index = 0;    // items before it
   int4 r0, r1;           // the next item's record
-  int64_t at = 0;
   __device__ __forceinline__ explicit Walk(const AttnArgs &args)
-      : a(args), n((int64_t)args.plan[AttnPlan::kUnits] * args.s.Hkv) { fetch(); }
+      : a(args), n((uint32_t)args.plan[AttnPlan::kUnits] * (uint32_t)args.s.Hkv) { fetch(); }
   __device__ __forceinline__ void fetch() {
-    const int64_t c = (k & 1) ? (int64_t)gridDim.x - 1 - blockIdx.x : (int64_t)blockIdx.x;
-    at = k * gridDim.x + c;
+    at = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
     if (at < n) {
-      const int4 *p = reinterpret_cast<const int4 *>(a.plan + a.p.units() + AttnPlan::kUnit * (at / a.s.Hkv));
+      const int4 *p = reinterpret_cast<const int4 *>(a.plan + a.p.units() + (int64_t)AttnPlan::kUnit * (at / (uint32_t)a.s.Hkv));
       r0 = p[0];
       r1 = p[1];
     }
@@ -158,24 +191,20 @@ struct Walk {
   __device__ __forceinline__ bool item(Item &it) {
     if (at >= n) return false;
     it.u = AttnUnit{r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-    it.head = (int)(at % a.s.Hkv);
+    it.head = (int)(at % (uint32_t)a.s.Hkv);
     it.blocks = it.u.kb1 - it.u.kb0;
     it.pair = it.u.tokens > a.s.tile_tokens;
-    it.steps = it.pair ? 2 * it.blocks : it.blocks;
     ++k;
     fetch();
     return true;
   }
   __device__ __forceinline__ void done(const Item &it) {
-    g += it.steps;
+    pos += it.blocks;
     ++index;
   }
-  // The first step of stream t in the item, and how many it has.
-  __device__ __forceinline__ int first(int t) const { return (int)((g ^ (uint32_t)t) & 1u); }
-  __device__ __forceinline__ int count(const Item &it, int t) const {
-    const int i = first(t);
-    return i < it.steps ? (it.steps - i + 1) / 2 : 0;
-  }
+  // Stream t's blocks of the item: from first(t) on, every step(it)-th one.
+  __device__ __forceinline__ int first(const Item &it, int t) const { return it.pair ? 0 : (int)((pos ^ (uint32_t)t) & 1u); }
+  __device__ __forceinline__ int step(const Item &it) const { return it.pair ? 1 : 2; }
 };
 
 // Keys that every row of a unit sees.
@@ -189,43 +218,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   extern __shared__ unsigned char smem_raw[];
   unsigned char *sm = align1024(smem_raw);
   uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + S::kBarOff);  // a K block is in
-  uint64_t *kfree = kfull + S::kK;       // its MMAs are done
+  uint64_t *kfree = kfull + S::kK;       // both streams' MMAs on it are done
   uint64_t *vfull = kfree + S::kK;       // a V block is in
-  uint64_t *vfree = vfull + S::kV;       // its MMAs are done
+  uint64_t *vfree = vfull + S::kV;       // both streams' MMAs on it are done
   uint64_t *fixed = vfree + S::kV;       // it has been looked at
   uint64_t *qfull = fixed + S::kV;       // a stream's Q tile is in
-  uint64_t *qfree = qfull + 2;           // its last score product is done
+  uint64_t *qfree = qfull + 2;           // its last scores are done
   uint64_t *sfull = qfree + 2;           // S of a stream's step is in TMEM
-  uint64_t *pfull = sfull + 2;           // P of it is
-  uint64_t *ofull = pfull + 2;           // a stream's last product with V is done
-  uint64_t *mfull = ofull + 2;           // the statistics of the stream to merge are in shared memory
+  uint64_t *pfull = sfull + 2;           // [stream][half]: P of it is
+  uint64_t *ofull = pfull + 4;           // a stream's last product with V is done
+  uint64_t *fin = ofull + 2;             // [stream]
+  uint64_t *go = fin + 2;                // [stream]: its turn to issue a step's MMAs
+  uint64_t *mfull = go + 2;              // the statistics of the stream to merge are in shared memory
   uint64_t *mfree = mfull + 1;           // its O has been read
-  uint64_t *fin = mfree + 1;
-  uint32_t *tslot = reinterpret_cast<uint32_t *>(fin + 1);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(mfree + 1);
   volatile int32_t *flags = reinterpret_cast<int32_t *>(tslot + 1);  // [item % kFlags]: the last item with values taken out
+  volatile uint32_t *reached = const_cast<volatile uint32_t *>(reinterpret_cast<volatile uint32_t *>(flags + kFlags));
   float2 *stats = reinterpret_cast<float2 *>(sm + S::kStatOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S::kK; ++i) {
+    for (uint32_t i = 0; i < S::kK; ++i) {
       mbar_init(&kfull[i], 1);
-      mbar_init(&kfree[i], 1);
+      mbar_init(&kfree[i], 2);
     }
-    for (int i = 0; i < S::kV; ++i) {
+    for (uint32_t i = 0; i < S::kV; ++i) {
       mbar_init(&vfull[i], 1);
-      mbar_init(&vfree[i], 1);
-      mbar_init(&fixed[i], 1);
+      mbar_init(&vfree[i], 2);
+      mbar_init(&fixed[i], kFixWarps);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&qfull[t], 1);
       mbar_init(&qfree[t], 1);
       mbar_init(&sfull[t], 1);
-      mbar_init(&pfull[t], 4);
+      mbar_init(&pfull[2 * t], 4);
+      mbar_init(&pfull[2 * t + 1], 4);
       mbar_init(&ofull[t], 1);
+      mbar_init(&fin[t], 1);
+      mbar_init(&go[t], 1);
     }
     mbar_init(mfull, 4);
     mbar_init(mfree, 4);
-    mbar_init(fin, 1);
     for (int i = 0; i < kFlags; ++i) flags[i] = -1;
+    reached[0] = reached[1] = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(tslot, S::kTmemCols);
@@ -240,10 +274,94 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   Walk w(a);
   Item it;
 
-  // The softmax warps hold a row of S: registers of the others' share go to them (2 * 216 + 72 = 3 * 168).
   if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == kKWarp || warp == kVWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp < kKWarp) {
+      // ---- MMAs of stream t
+      constexpr uint32_t id_s = idesc_kk(kRows, kKeyBlock), id_o = idesc_bf16(kRows, D);
+      const int t = warp - kMmaWarp;
+      const uint32_t ts = tmem + S::kS + t * 128, to = tmem + S::kO + t * 128;
+      const uint64_t qd = smem_desc(smem_addr(sm + t * S::kTileBytes), 16, 1024, kSw128);
+      const uint64_t kd = smem_desc(smem_addr(sm + S::kKOff), 16, 1024, kSw128);
+      const uint64_t vd = smem_desc(smem_addr(sm + S::kVOff), S::kHalfBytes, 1024, kSw128);
+      Walk ws(a);          // of the scores, a step ahead
+      Item is{};
+      int sb = 0;          // their next block in the item
+      uint32_t items = 0, steps = 0, turns = t == 0 ? 1 : 0;
+      uint64_t *kfree_next = kfree;
+      uint32_t own = ~0u;  // slots whose last K block this stream has used (or none has been in)
+      bool more = ws.item(is);
+      if (more) sb = ws.first(is, t);
+      // The next step's scores, in two parts so that nothing but MMAs stands between a step's products: its operands, and
+      // its MMAs.
+      uint64_t kd_next = 0;
+      auto operands = [&]() -> bool {
+        while (more && sb >= is.blocks) {
+          if (ws.first(is, t ^ 1) < is.blocks && !is.pair) own &= t == 0 ? 0x55555555u : 0xaaaaaaaau;
+          ws.done(is);
+          more = ws.item(is);
+          if (more) sb = ws.first(is, t);
+        }
+        const uint32_t pos = more ? ws.pos + sb : ~0u, slot = pos % S::kK;
+        if (lane == 0) reached[t] = pos;  // every K block of this stream before it has been in
+        if (!more) return true;
+        // A barrier's phases are told apart by their parity only. Where the slot's last block was the other stream's alone,
+        // that one has to have been in before this stream may wait for the next.
+        if ((own >> slot & 1) == 0 && !__all_sync(0xffffffffu, past(&reached[t ^ 1], pos - S::kK, a.err, kErrAttn)))
+          return false;
+        own |= 1u << slot;
+        if (sb < ws.step(is) && !await(&qfull[t], items++ & 1, a.err, kErrAttn)) return false;
+        if (!await(&kfull[slot], pos / S::kK & 1, a.err, kErrAttn)) return false;
+        kd_next = kd + slot * (S::kTileBytes >> 4);
+        kfree_next = &kfree[slot];
+        return true;
+      };
+      auto scores = [&]() {
+#pragma unroll
+        for (int h = 0; h < S::kHalves; ++h)
+          mma_run<4>(ts, qd + h * (S::kHalfBytes >> 4), kd_next + h * (S::kHalfBytes >> 4), 2, 2, id_s, h > 0);
+        mma_commit_elect(&sfull[t]);
+      };
+      auto scores_done = [&]() {  // behind scores(): what its end releases
+        mma_commit_elect(kfree_next);
+        if (!is.pair) mma_commit_elect(kfree_next);  // for the other stream
+        sb += ws.step(is);
+        if (sb >= is.blocks) mma_commit_elect(&qfree[t]);
+      };
+      bool ok = operands();
+      tc_after_sync();
+      if (ok && more) {
+        scores();
+        scores_done();
+      }
+      while (ok && w.item(it)) {
+        const int d = w.step(it), b0 = w.first(it, t);
+        for (int b = b0; b < it.blocks; b += d, ++steps) {
+          const uint32_t pos = w.pos + b, slot = pos % S::kV;
+          const uint64_t vd_now = vd + slot * (S::kTileBytes >> 4);
+          if (!(ok = operands() && await(&fixed[slot], pos / S::kV & 1, a.err, kErrAttn) &&
+                     await(&pfull[2 * t], steps & 1, a.err, kErrAttn)))
+            break;
+          // Streams of two tiles take turns: left alone they fall into step, and the tensor core idles while both take
+          // exponentials.
+          if (it.pair && !await(&go[t], turns++ & 1, a.err, kErrAttn)) { ok = false; break; }
+          tc_after_sync();
+          mma_pv4(to, ts, vd_now, 128, id_o, b != b0);  // 64 keys
+          if (!await(&pfull[2 * t + 1], steps & 1, a.err, kErrAttn)) { ok = false; break; }
+          tc_after_sync();
+          mma_pv4(to, ts + 32, vd_now + (64 * 128 >> 4), 128, id_o, 1);
+          if (b + d >= it.blocks) mma_commit_elect(&ofull[t]);
+          if (more) scores();
+          if (it.pair && lane == 0) mbar_arrive(&go[t ^ 1]);
+          mma_commit_elect(&vfree[slot]);
+          if (!it.pair) mma_commit_elect(&vfree[slot]);
+          if (more) scores_done();
+        }
+        w.done(it);
+      }
+      mma_commit_elect(&fin[t]);
+      await(&fin[t], 0, a.err, kErrAttn);  // every MMA is done before TMEM is freed
+    } else if (warp < kFixWarp) {
       // ---- loads: one warp K blocks and Q tiles, one V blocks
       const bool keys = warp == kKWarp;
       const uint32_t n_slots = keys ? S::kK : S::kV;
@@ -251,10 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const CUtensorMap *map = keys ? &maps.k : &maps.v;
       unsigned char *ring = sm + (keys ? S::kKOff : S::kVOff);
       const int half = lane % S::kHalves, part = lane / S::kHalves;
-      uint32_t slot = 0, phase = 0, used[2] = {0, 0};
+      uint32_t slot = 0, phase = 0, used0 = 0, used1 = 0;
       bool ok = true;
       while (ok && w.item(it)) {
-        const int64_t row0 = (int64_t)it.u.row0 - it.u.pos0;  // packed rows: the sequence's first
         for (int b = 0; b < it.blocks; ++b) {
           const int j0 = (it.u.kb0 + b) * kKeyBlock;
           int page = 0, copies = S::kHalves, in_page = 0, rows = kKeyBlock;  // copies of a block, rows of each
@@ -273,13 +390,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               }
             }
           }
-          if (!mbar_wait_warp(&free[slot], phase ^ 1, a.err, kErrAttn)) { ok = false; break; }
+          if (!await(&free[slot], phase ^ 1, a.err, kErrAttn)) { ok = false; break; }
           if (lane == 0) mbar_arrive_tx(&full[slot], (uint32_t)(copies * rows * 128));
           __syncwarp();
           unsigned char *dst = ring + slot * S::kTileBytes + half * S::kHalfBytes;
           if (lane < copies) {
             if constexpr (PAGED) tma_load_4d(dst + part * rows * 128, map, half * 64, in_page, it.head, page, &full[slot]);
-            else tma_load_3d(dst, map, half * 64, it.head, (int)(row0 + j0), &full[slot]);
+            else tma_load_3d(dst, map, half * 64, it.head, it.u.row0 - it.u.pos0 + j0, &full[slot]);
           }
           if (++slot == n_slots) {
             slot = 0;
@@ -290,239 +407,182 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           // stream's own where there are two, the same for both where there is one.
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (!ok || w.count(it, t) == 0) continue;
-            if (!mbar_wait_warp(&qfree[t], (used[t] & 1) ^ 1, a.err, kErrAttn)) { ok = false; continue; }
-            ++used[t];
+            uint32_t &used = t == 0 ? used0 : used1;
+            if (!ok || w.first(it, t) >= it.blocks) continue;
+            if (!await(&qfree[t], (used & 1) ^ 1, a.err, kErrAttn)) { ok = false; continue; }
+            ++used;
             if (lane == 0) mbar_arrive_tx(&qfull[t], (uint32_t)(S::kHalves * a.s.tile_tokens * a.s.G * 128));
             __syncwarp();
             if (lane < S::kHalves)
               tma_load_3d(sm + t * S::kTileBytes + lane * S::kHalfBytes, &maps.q, lane * 64, it.head * a.s.G,
-                          it.u.row0 + (it.pair ? w.first(t) * a.s.tile_tokens : 0), &qfull[t]);
+                          it.u.row0 + (it.pair ? t * a.s.tile_tokens : 0), &qfull[t]);
           }
           if (!ok) break;
         }
         w.done(it);
       }
-    } else if (warp == kFixWarp) {
-      // ---- values that not every row sees
+    } else {
+      // ---- values that not every row sees: each warp looks at every kFixWarps-th group of 32 chunks of 16 bytes
+      constexpr int kChunks = D / 8;  // of a row
+      const int me = (warp - kFixWarp) * 32 + lane;
       uint32_t slot = 0, phase = 0;
       bool ok = true;
       while (ok && w.item(it)) {
         const int seen = common_keys(it.u, a.s.causal);
-        for (int b = 0; b < it.blocks && ok; ++b) {
-          const uint32_t v = slot;
+        for (int b = 0; b < it.blocks; ++b) {
           const int j0 = (it.u.kb0 + b) * kKeyBlock;
-          if (!mbar_wait_warp(&vfull[v], phase, a.err, kErrAttn)) { ok = false; break; }
+          if (!await(&vfull[slot], phase, a.err, kErrAttn)) { ok = false; break; }
+          if (j0 + kKeyBlock > seen) {
+            unsigned char *base = sm + S::kVOff + slot * S::kTileBytes;
+            auto chunk = [&](int i) {
+              const int r = i / kChunks, c = i % kChunks;
+              return reinterpret_cast<uint4 *>(base + (c / 8) * S::kHalfBytes + swz128(r, c % 8));
+            };
+            const int i0 = max(0, seen - j0) * kChunks, i1 = min(kKeyBlock, it.u.kv_len - j0) * kChunks;  // looked at; zeroed from i1 on
+            uint32_t any = 0;  // an exponent of all ones, plus one, carries into its sign
+#pragma unroll 4
+            for (int i = i0 + me; i < i1; i += 32 * kFixWarps) {
+              const uint4 x = *chunk(i);
+              any |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                     ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+            }
+            if (any & 0x80008000u) {
+              flags[w.index % kFlags] = (int)w.index;
+              for (int i = i0 + me; i < i1; i += 32 * kFixWarps) {
+                const uint4 x = *chunk(i);
+                uint32_t q[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if ((q[e] & 0x7f80u) == 0x7f80u) q[e] &= 0xffff0000u;
+                  if ((q[e] & 0x7f800000u) == 0x7f800000u) q[e] &= 0xffffu;
+                }
+                *chunk(i) = make_uint4(q[0], q[1], q[2], q[3]);
+              }
+            }
+            for (int i = i1 + me; i < kKeyBlock * kChunks; i += 32 * kFixWarps) *chunk(i) = make_uint4(0, 0, 0, 0);
+            fence_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&fixed[slot]);
           if (++slot == S::kV) {
             slot = 0;
             phase ^= 1;
           }
-          if (j0 + kKeyBlock <= seen) {
-            if (lane == 0) mbar_arrive(&fixed[v]);
-            continue;
-          }
-          unsigned char *base = sm + S::kVOff + v * S::kTileBytes;
-          const int r0 = max(0, seen - j0), r1 = min(kKeyBlock, it.u.kv_len - j0);  // looked at; zeroed from r1 on
-          bool any = false;
-          for (int i = lane; i < (r1 - r0) * (D / 8); i += 32) {
-            const int r = r0 + i / (D / 8), c = i % (D / 8);
-            uint4 *p = reinterpret_cast<uint4 *>(base + (c / 8) * S::kHalfBytes + swz128(r, c % 8));
-            const uint4 x = *p;
-            uint32_t q[4] = {x.x, x.y, x.z, x.w};
-            bool bad = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {  // exponents of all ones
-              if ((q[e] & 0x7f80u) == 0x7f80u) { q[e] &= 0xffff0000u; bad = true; }
-              if ((q[e] & 0x7f800000u) == 0x7f800000u) { q[e] &= 0xffffu; bad = true; }
-            }
-            if (bad) {
-              *p = make_uint4(q[0], q[1], q[2], q[3]);
-              any = true;
-            }
-          }
-          for (int i = lane; i < (kKeyBlock - r1) * (D / 8); i += 32) {
-            const int r = r1 + i / (D / 8), c = i % (D / 8);
-            *reinterpret_cast<uint4 *>(base + (c / 8) * S::kHalfBytes + swz128(r, c % 8)) = make_uint4(0, 0, 0, 0);
-          }
-          if (any) flags[w.index % kFlags] = (int)w.index;
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&fixed[v]);
         }
         w.done(it);
       }
-    } else {
-      // ---- MMA issue. The score products run two steps ahead of the others, over units' ends as well.
-      constexpr uint32_t id_s = idesc_kk(kRows, kKeyBlock), id_o = idesc_bf16(kRows, D);
-      Walk ws(a);  // of the score products
-      Item is{};
-      int si = 0;  // their next step in it
-      bool more = ws.item(is), ok = true;
-      uint32_t sslot = 0, sphase = 0;    // slot of its K block
-      uint32_t qused[2] = {0, 0}, pused[2] = {0, 0};
-      uint32_t slot = 0, phase = 0;      // slot of the other products' V block
-      auto scores = [&]() -> bool {  // the next step's scores
-        while (more && si == is.steps) {
-          ws.done(is);
-          more = ws.item(is);
-          si = 0;
-        }
-        if (!more) return true;
-        const int t = (int)((ws.g + si) & 1u);
-        if (si < 2) {
-          if (!mbar_wait_warp(&qfull[t], qused[t] & 1, a.err, kErrAttn)) return false;
-          ++qused[t];
-        }
-        if (!is.pair || (si & 1) == 0)
-          if (!mbar_wait_warp(&kfull[sslot], sphase, a.err, kErrAttn)) return false;
-        tc_after_sync();
-        const uint32_t q = smem_addr(sm + t * S::kTileBytes), k = smem_addr(sm + S::kKOff + sslot * S::kTileBytes);
-#pragma unroll
-        for (int h = 0; h < S::kHalves; ++h)
-          mma_run<4>(tmem + S::kS + t * 128, smem_desc(q + h * S::kHalfBytes, 16, 1024, kSw128),
-                     smem_desc(k + h * S::kHalfBytes, 16, 1024, kSw128), 2, 2, id_s, h > 0);
-        mma_commit_elect(&sfull[t]);
-        if (si + 2 >= is.steps) mma_commit_elect(&qfree[t]);
-        if (!is.pair || (si & 1) == 1) {
-          mma_commit_elect(&kfree[sslot]);
-          if (++sslot == S::kK) {
-            sslot = 0;
-            sphase ^= 1;
-          }
-        }
-        ++si;
-        return true;
-      };
-      ok = scores() && scores();
-      while (ok && w.item(it)) {
-        for (int i = 0; i < it.steps && ok; ++i) {
-          const int t = (int)((w.g + i) & 1u);
-          if (!it.pair || (i & 1) == 0)
-            if (!mbar_wait_warp(&fixed[slot], phase, a.err, kErrAttn)) { ok = false; break; }
-          if (!mbar_wait_warp(&pfull[t], pused[t] & 1, a.err, kErrAttn)) { ok = false; break; }
-          ++pused[t];
-          tc_after_sync();
-          const uint32_t vs = smem_addr(sm + S::kVOff + slot * S::kTileBytes);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)  // 64 keys each
-            mma_pv4(tmem + S::kO + t * 128, tmem + S::kS + t * 128 + h * 32,
-                    smem_desc(vs + h * 64 * 128, S::kHalfBytes, 1024, kSw128), 128, id_o, i >= 2 || h > 0);
-          if (i + 2 >= it.steps) mma_commit_elect(&ofull[t]);
-          if (!it.pair || (i & 1) == 1) {
-            mma_commit_elect(&vfree[slot]);
-            if (++slot == S::kV) {
-              slot = 0;
-              phase ^= 1;
-            }
-          }
-          ok = scores();
-        }
-        w.done(it);
-      }
-      mma_commit_elect(fin);
-      mbar_wait_warp(fin, 0, a.err, kErrAttn);  // every MMA is done before TMEM is freed
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---- softmax of stream t, a thread a row
     const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const uint32_t ts = tmem + lanes + S::kS + t * 128, to = tmem + lanes + S::kO;
+    const uint32_t ts = tmem + lanes + S::kS + t * 128, to = tmem + lanes + S::kO + t * 128;
+    const uint32_t to_other = tmem + lanes + S::kO + (t ^ 1) * 128;
+    unsigned char *turn = sm + S::kTurnOff + warp * S::kTurnBytes;
     const float c = a.s.scale_log2;
-    uint32_t sused = 0, oused[2] = {0, 0}, merges = 0;
+    const int tile_rows = a.s.tile_tokens * a.s.G, row_tok = r / a.s.G, row_head = r % a.s.G;
+    uint32_t steps = 0, mine_used = 0, other_used = 0, merges = 0;
     bool ok = true;
     while (ok && w.item(it)) {
-      const int i0 = w.first(t), mine = w.count(it, t), other = w.count(it, t ^ 1);
-      const bool writes = it.pair || i0 == 0;  // the stream whose warpgroup stores the rows
-      // The row: its token and head, and the keys it sees.
-      const int tile = it.pair ? i0 : 0, tok = tile * a.s.tile_tokens + r / a.s.G;
-      const bool live = r < a.s.tile_tokens * a.s.G && tok < it.u.tokens;
+      const int d = w.step(it), b0 = w.first(it, t);
+      const bool mine = b0 < it.blocks, other = w.first(it, t ^ 1) < it.blocks;
+      const bool writes = it.pair || b0 == 0;  // the stream whose warpgroup stores the rows
+      // The row: its token, and the keys it sees.
+      const int tile = it.pair ? t : 0, tok = tile * a.s.tile_tokens + row_tok;
+      const bool live = r < tile_rows && tok < it.u.tokens;
       const bool busy = __any_sync(0xffffffffu, live);
       const int lim = live ? visible_keys(it.u.pos0 + tok, it.u.kv_len, a.s.causal) : INT32_MAX / 2;
       float m = -INFINITY, l = 0.f;  // of c * s
-      for (int n = 0; n < mine && ok; ++n) {
-        const int i = i0 + 2 * n, j0 = (it.u.kb0 + (it.pair ? i >> 1 : i)) * kKeyBlock;
-        if (!mbar_wait_warp(&sfull[t], sused & 1, a.err, kErrAttn)) { ok = false; break; }
-        ++sused;
-        if (busy) {
-          tc_after_sync();
-          float s[128];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) tmem_ld32_async(ts + 32 * x, s + 32 * x);
-          tmem_wait_ld();
-          const int sees = lim - j0;
-          if (__any_sync(0xffffffffu, sees < kKeyBlock)) {
-#pragma unroll
-            for (int x = 0; x < 128; ++x) s[x] = x < sees ? s[x] : -INFINITY;
-          }
-          float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int x = 4; x < 128; ++x) top[x & 3] = fmaxf(top[x & 3], s[x]);
-          const float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-          const bool rise = mn > m + kLazy;
-          if (__any_sync(0xffffffffu, rise)) {
-            const float up = rise ? ex2(m - mn) : 1.f;
-            if (rise) m = mn;
-            l *= up;
-            if (n > 0) {
-#pragma unroll 1
-              for (int x = 0; x < D; x += 16) {
-                float o[16];
-                tmem_ld16(to + t * 128 + x, o);
-#pragma unroll
-                for (int y = 0; y < 16; ++y) o[y] *= up;
-                tmem_st16(to + t * 128 + x, o);
-              }
-            }
-          }
-          const float base = m == -INFINITY ? 0.f : m;
-          const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t p[32];
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              float2 e = fma2(make_float2(s[64 * h + 2 * x], s[64 * h + 2 * x + 1]), c2, b2);
-              e.x = ex2(e.x);
-              e.y = ex2(e.y);
-              sum[x & 1] = add2(sum[x & 1], e);
-              p[x] = pack_bf16(e.x, e.y);
-            }
-            tmem_st32(ts + 32 * h, p);
-          }
-          sum[0] = add2(sum[0], sum[1]);
-          l += sum[0].x + sum[0].y;
-          tmem_wait_st();
-          tc_before_sync();
+      for (int b = b0; b < it.blocks; b += d, ++steps) {
+        if (!await(&sfull[t], steps & 1, a.err, kErrAttn)) { ok = false; break; }
+        if (!busy) {
+          if (lane < 2) mbar_arrive(&pfull[2 * t + lane]);
+          continue;
         }
+        tc_after_sync();
+        float s[128];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_ld32_async(ts + 32 * x, s + 32 * x);
+        tmem_wait_ld();
+        const int sees = lim - (it.u.kb0 + b) * kKeyBlock;
+        if (__any_sync(0xffffffffu, sees < kKeyBlock)) {
+#pragma unroll
+          for (int x = 0; x < 128; ++x) s[x] = x < sees ? s[x] : -INFINITY;
+        }
+        float top[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top[x] = max3(s[x], s[x + 4], s[x + 8]);
+#pragma unroll
+        for (int x = 12; x < 124; x += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) top[y] = max3(top[y], s[x + y], s[x + y + 4]);
+        const float mn = max3(max3(top[0], top[1], s[124]), max3(top[2], top[3], s[125]), fmaxf(s[126], s[127])) * c;
+        const bool rise = mn > m + kLazy;
+        if (__any_sync(0xffffffffu, rise)) {
+          const float up = rise ? ex2(m - mn) : 1.f;
+          if (rise) m = mn;
+          l *= up;
+          if (b != b0) {
+#pragma unroll 1
+            for (int x = 0; x < D; x += 16) {
+              float o[16];
+              tmem_ld16(to + x, o);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] *= up;
+              tmem_st16(to + x, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+        const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t p[32];
+        auto weight = [&](int x, int y) {  // weights 2 x and 2 x + 1 of the row, to p[y]
+          float2 e = fma2(make_float2(s[2 * x], s[2 * x + 1]), c2, b2);
+          e.x = ex2(e.x);
+          e.y = ex2(e.y);
+          sum[x & 1] = add2(sum[x & 1], e);
+          p[y] = pack_bf16(e.x, e.y);
+        };
+#pragma unroll
+        for (int x = 0; x < 32; ++x) weight(x, x);
+        tmem_st32(ts, p);
+        tmem_wait_st();
+        tc_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[t]);
+        if (lane == 0) mbar_arrive(&pfull[2 * t]);
+#pragma unroll
+        for (int x = 0; x < 32; ++x) weight(32 + x, x);
+        tmem_st32(ts + 32, p);
+        tmem_wait_st();
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[2 * t + 1]);
+        sum[0] = add2(sum[0], sum[1]);
+        l += sum[0].x + sum[0].y;
       }
       if (!ok) break;
       // ---- the end of the unit
-      const bool merge = !it.pair && other > 0 && mine > 0;
+      const bool merge = !it.pair && other && mine;
       if (!writes) {
-        oused[t] += mine > 0;
-        oused[t ^ 1] += other > 0;
+        mine_used += mine;
+        other_used += other;
         if (merge) {
           stats[r] = make_float2(m, l);
           __syncwarp();
           if (lane == 0) mbar_arrive(mfull);
-          if (!mbar_wait_warp(mfree, merges & 1, a.err, kErrAttn)) { ok = false; break; }
+          if (!await(mfree, merges & 1, a.err, kErrAttn)) { ok = false; break; }
           ++merges;
         }
         w.done(it);
         continue;
       }
+      if (mine && !await(&ofull[t], mine_used & 1, a.err, kErrAttn)) { ok = false; break; }
+      mine_used += mine;
       float w0 = 1.f, w1 = 0.f;  // weights of this stream's and the other's O
-      if (mine > 0) {
-        if (!mbar_wait_warp(&ofull[t], oused[t] & 1, a.err, kErrAttn)) { ok = false; break; }
-        ++oused[t];
-      }
       if (merge) {
-        if (!mbar_wait_warp(&ofull[t ^ 1], oused[t ^ 1] & 1, a.err, kErrAttn) ||
-            !mbar_wait_warp(mfull, merges & 1, a.err, kErrAttn)) { ok = false; break; }
+        if (!await(&ofull[t ^ 1], other_used & 1, a.err, kErrAttn) || !await(mfull, merges & 1, a.err, kErrAttn)) { ok = false; break; }
         ++merges;
         const float2 o = stats[r];
         const float mm = fmaxf(m, o.x), base = mm == -INFINITY ? 0.f : mm;
@@ -531,37 +591,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         l = l * w0 + o.y * w1;
         m = mm;
       }
-      oused[t ^ 1] += other > 0;
+      other_used += other;
       tc_after_sync();
-      const int64_t row = (int64_t)it.u.row0 + tok;
-      const int head = it.head * a.s.G + r % a.s.G;
-      const bool split = it.u.slot >= 0, some = it.steps > 0;
-      const float inv = split ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      w0 *= inv;
-      w1 *= inv;
-      const bool taken = some && flags[w.index % kFlags] == (int)w.index;
       if (busy) {
-        float *part = nullptr;
-        if (split) part = a.ws + ((int64_t)it.u.slot * a.s.Hkv + it.head) * slot_floats(a.s);
-        const int unit_row = tile * a.s.tile_tokens * a.s.G + r;
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + row * a.ldo + (int64_t)head * D;
+        const int64_t row = (int64_t)it.u.row0 + tok;
+        const int head = it.head * a.s.G + row_head;
+        const bool split = it.u.slot >= 0;
+        const float inv = split ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        w0 *= inv;
+        w1 *= inv;
+        const bool taken = mine && live && flags[w.index % kFlags] == (int)w.index;
+        // The row's address (nothing there for rows that are none), and what a warp turns round at a time: 128 bytes a row.
+        unsigned char *dst = nullptr;
+        if (live && split) {
+          float *part = a.ws + ((int64_t)it.u.slot * a.s.Hkv + it.head) * slot_floats(a.s);
+          const int unit_row = tile * tile_rows + r;
+          dst = reinterpret_cast<unsigned char *>(part + (int64_t)unit_row * D);
+          *reinterpret_cast<float2 *>(part + (int64_t)a.s.slot_rows * D + 2 * unit_row) = make_float2(m, l);
+        } else if (live) {
+          dst = reinterpret_cast<unsigned char *>(static_cast<__nv_bfloat16 *>(a.out) + row * a.ldo + (int64_t)head * D);
+          if (a.lse != nullptr) a.lse[row * a.s.Hq + head] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+        }
+        const uint64_t mine_at = reinterpret_cast<uint64_t>(dst);
 #pragma unroll 1
         for (int x = 0; x < D; x += 32) {
           float o[32];
-          if (some) {
-            tmem_ld32_async(to + t * 128 + x, o);
+          if (mine) {
+            tmem_ld32_async(to + x, o);
             tmem_wait_ld();
           }
 #pragma unroll
-          for (int y = 0; y < 32; ++y) o[y] = some ? o[y] * w0 : 0.f;
+          for (int y = 0; y < 32; ++y) o[y] = mine ? o[y] * w0 : 0.f;
           if (merge) {
             float o1[32];
-            tmem_ld32_async(to + (t ^ 1) * 128 + x, o1);
+            tmem_ld32_async(to_other + x, o1);
             tmem_wait_ld();
 #pragma unroll
             for (int y = 0; y < 32; ++y) o[y] = fmaf(o1[y], w1, o[y]);
           }
-          if (taken && live) {
+          if (taken) {
             // Values that were taken out, for the rows that see them.
             const int end = min(lim, it.u.kb1 * kKeyBlock);
             for (int j = max(common_keys(it.u, a.s.causal), it.u.kb0 * kKeyBlock); j < end; ++j) {
@@ -581,23 +649,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
               }
             }
           }
-          if (live) {
-            if (split) {
-              float4 *d = reinterpret_cast<float4 *>(part + (int64_t)unit_row * D + x);
+          // To shared memory, 16-byte chunks rotated by the row, and out in whole 128-byte pieces of four rows: after each
+          // 32 columns of partial results, after each 64 of a result.
+          auto put = [&](int chunk, uint4 v) { *reinterpret_cast<uint4 *>(turn + lane * 128 + ((chunk ^ lane) & 7) * 16) = v; };
+          if (split) {
 #pragma unroll
-              for (int y = 0; y < 8; ++y) d[y] = make_float4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-            } else {
-              uint4 *d = reinterpret_cast<uint4 *>(out + x);
+            for (int y = 0; y < 8; ++y)
+              put(y, make_uint4(__float_as_uint(o[4 * y]), __float_as_uint(o[4 * y + 1]), __float_as_uint(o[4 * y + 2]),
+                                __float_as_uint(o[4 * y + 3])));
+          } else {
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                d[y] = make_uint4(pack_bf16(o[8 * y], o[8 * y + 1]), pack_bf16(o[8 * y + 2], o[8 * y + 3]),
-                                  pack_bf16(o[8 * y + 4], o[8 * y + 5]), pack_bf16(o[8 * y + 6], o[8 * y + 7]));
-            }
+            for (int y = 0; y < 4; ++y)
+              put((x >> 5 & 1) * 4 + y, make_uint4(pack_bf16(o[8 * y], o[8 * y + 1]), pack_bf16(o[8 * y + 2], o[8 * y + 3]),
+                                                   pack_bf16(o[8 * y + 4], o[8 * y + 5]), pack_bf16(o[8 * y + 6], o[8 * y + 7])));
+            if ((x & 32) == 0) continue;
           }
-        }
-        if (live) {
-          if (split) *reinterpret_cast<float2 *>(part + (int64_t)a.s.slot_rows * D + 2 * unit_row) = make_float2(m, l);
-          else if (a.lse != nullptr) a.lse[row * a.s.Hq + head] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+          __syncwarp();
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int rr = 4 * y + lane / 8, cc = lane & 7;
+            const uint64_t at = __shfl_sync(0xffffffffu, mine_at, rr);
+            const uint4 v = *reinterpret_cast<const uint4 *>(turn + rr * 128 + ((cc ^ rr) & 7) * 16);
+            if (at != 0) *reinterpret_cast<uint4 *>(at + (split ? x * 4 : (x & ~63) * 2) + cc * 16) = v;
+          }
+          __syncwarp();
         }
       }
       tc_before_sync();
