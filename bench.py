@@ -150,7 +150,7 @@ def load_peaks():
 
 
 # Sources of the mixture-of-experts layer around the LoRA: no workload here launches their kernels.
-UNBENCHED_SOURCES = ("attn.cuh", "attn_abi.cu", "attn_plan.cu", "attn_rows.cu", "attn_tc.cu", "moe_layer.cu", "moe_product.cu", "moe_product_tc.cu", "mx.cu", "mx.cuh")
+UNBENCHED_SOURCES = ("attn.cuh", "attn_abi.cu", "attn_few.cu", "attn_plan.cu", "attn_rows.cu", "attn_tc.cu", "attn_tc.cuh", "moe_layer.cu", "moe_product.cu", "moe_product_tc.cu", "mx.cu", "mx.cuh")
 
 
 def kernel_source_hash(csrc=os.path.join(ROOT, "rank_adapter_gb300", "csrc")):

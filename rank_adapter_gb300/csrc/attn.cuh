@@ -18,6 +18,7 @@ constexpr int kErrBadPage = 2;  // a page id outside the cache was met
 struct AttnShape {
   int dtype, Hq, Hkv, G, D, causal;
   bool tc;           // on the tensor cores
+  int few;           // rows of a unit of few rows (attn_few.cu), 0: units of up to two tiles (attn_tc.cu)
   int tile_tokens;   // tokens whose rows share one 128-row tile (tensor cores)
   int unit_tokens;   // most tokens of a unit
   int slot_rows;     // rows of a partial result
@@ -92,6 +93,7 @@ __host__ __device__ inline int64_t slot_floats(const AttnShape &s) { return (int
 
 AttnShape attn_shape(const lora_seqs &q);
 AttnPlan attn_plan(const AttnShape &s, int num_seqs, int num_tokens);
+size_t attn_plan_bytes(const lora_seqs &q);  // enough for up to so many sequences and rows, however units are cut
 bool attn_may_split(const AttnShape &s, int64_t max_kv);
 
 cudaError_t launch_prepare_seqs(const lora_seqs &q, cudaStream_t st);
@@ -99,6 +101,7 @@ cudaError_t launch_kv_write(const lora_seqs &q, const lora_kv_cache &c, const vo
                             int64_t ldv, cudaStream_t st);
 bool attn_tc_takes(const AttnShape &s);
 cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t st);       // tensor cores (attn_tc.cu)
+cudaError_t launch_attn_few(const AttnArgs &a, cudaStream_t st);      // the same, units of few rows over pages (attn_few.cu)
 cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t st);     // CUDA cores (attn_rows.cu)
 cudaError_t launch_attn_combine(const AttnArgs &a, cudaStream_t st);  // joins the partial results
 

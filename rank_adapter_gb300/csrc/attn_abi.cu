@@ -92,7 +92,10 @@ int run(const lora_seqs *s, ra::AttnArgs &a, const void *q, int64_t ldq, void *o
   a.ws = static_cast<float *>(ws);
   a.num_tokens = s->num_tokens;
   const int64_t max_kv = has_cache(s) ? (int64_t)s->page_size * s->max_pages : s->num_tokens;
-  cudaError_t e = a.s.tc ? ra::launch_attn_tc(a, (cudaStream_t)stream) : ra::launch_attn_rows(a, (cudaStream_t)stream);
+  const cudaStream_t st_ = (cudaStream_t)stream;
+  cudaError_t e = a.s.few > 0 && a.kv.page_size > 0 ? ra::launch_attn_few(a, st_)
+                  : a.s.tc                          ? ra::launch_attn_tc(a, st_)
+                                                    : ra::launch_attn_rows(a, st_);
   if (e == cudaSuccess && ra::attn_may_split(a.s, max_kv)) e = ra::launch_attn_combine(a, (cudaStream_t)stream);
   return cuda_status(e);
 }
@@ -103,13 +106,14 @@ extern "C" {
 
 size_t lora_seqs_plan_bytes(const lora_seqs *seqs) {
   if (check_shape(seqs) != LORA_OK) return 0;
-  return (size_t)ra::attn_plan(ra::attn_shape(*seqs), seqs->num_seqs, seqs->num_tokens).words() * sizeof(int32_t);
+  return ra::attn_plan_bytes(*seqs);
 }
 
 size_t lora_attn_workspace_bytes(const lora_seqs *seqs) {
   if (check_shape(seqs) != LORA_OK) return 0;
   const ra::AttnShape s = ra::attn_shape(*seqs);
-  return (size_t)s.max_slots * s.Hkv * ra::slot_floats(s) * sizeof(float);
+  const int64_t rows = s.tc ? 256 : s.slot_rows;  // whichever way units are cut
+  return (size_t)(s.max_slots * s.Hkv * rows * (s.D + 2)) * sizeof(float);
 }
 
 int lora_prepare_seqs(const lora_seqs *seqs, lora_stream_t stream) {

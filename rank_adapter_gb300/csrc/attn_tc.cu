@@ -24,8 +24,7 @@
 // looked at by warps of their own before the MMA, since 0 * NaN is NaN: rows behind
 // the keys are zeroed, and where a later token's value is not finite it is taken out and
 // added to the rows that see it at the end.
-#include "attn.cuh"
-#include "tcgen05.cuh"
+#include "attn_tc.cuh"
 
 namespace ra {
 namespace {
@@ -63,152 +62,6 @@ struct TcMaps {
   CUtensorMap q;     // {D, heads, rows}, boxes of 64 x group x tile tokens
   CUtensorMap k, v;  // packed rows: {D, heads, rows}, boxes of 64 x 1 x 128; pages: {D, keys of a page, heads, pages}, 64 x keys x 1 x 1
 };
-
-// ------------------------------------------------------------------ PTX
-
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
-      : "memory");
-}
-__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-// Four MMAs of 16 keys each: A (P) in TMEM, 8 columns a step, B (V) in shared memory. Every lane of the warp calls it.
-__device__ __forceinline__ void mma_pv4(uint32_t d, uint32_t p, uint64_t bd, uint64_t b_step, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred q, e, t;\n\t.reg .b32 r, a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
-      "elect.sync r|e, 0xffffffff;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 t, %3, %3;\n\t"
-      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
-      "add.s64 b1, %2, %5;\n\tadd.s64 b2, b1, %5;\n\tadd.s64 b3, b2, %5;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}"
-      ::"r"(d), "r"(p), "l"(bd), "r"(idesc), "r"(acc), "l"(b_step) : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
-      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
-        "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
-      ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
-        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float x, float y, float z) {
-  float m;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
-  return m;
-}
-// Two fp32 operations an instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-// kind::f16 with fp32 accumulator and both operands K-major.
-__host__ __device__ constexpr uint32_t idesc_kk(int M, int N) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-// mbar_wait_warp, but for its first look at the clock: reading %globaltimer takes longer than most of these waits.
-__device__ __forceinline__ bool await(uint64_t *b, uint32_t parity, int *err, int code) {
-  bool ok = mbar_try(b, parity);
-  for (int i = 0; !ok && i < 32; ++i) ok = mbar_try(b, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  return mbar_wait_warp(b, parity, err, code);
-}
-
-// Waits, for up to kWaitNs, until *at is past pos.
-__device__ __forceinline__ bool past(const volatile uint32_t *at, uint32_t pos, int *err, int code) {
-  const uint64_t t0 = *at > pos ? 0 : global_ns();
-  while (*at <= pos)
-    if (global_ns() - t0 > kWaitNs) {
-      atomicOr(err, code);
-      return false;
-    }
-  __threadfence_block();
-  return true;
-}
-
-// ------------------------------------------------------------------ walk over a CTA's items
-
-// Item k of this CTA (a unit of one key-value head): the units lie in order of falling cost; every other round of
-// CTAs runs backwards.
-struct Item {
-  AttnUnit u;
-  int head, blocks;
-  bool pair;
-};
-
-struct Walk {
-  const AttnArgs &a;
-  uint32_t n, at, k = 0;
-  uint32_t pos = 0;      // blocks before the current item: block b of one tile belongs to stream (pos + b) & 1
-  uint32_t index = 0;    // items before it
-  int4 r0, r1;           // the next item's record
-  __device__ __forceinline__ explicit Walk(const AttnArgs &args)
-      : a(args), n((uint32_t)args.plan[AttnPlan::kUnits] * (uint32_t)args.s.Hkv) { fetch(); }
-  __device__ __forceinline__ void fetch() {
-    at = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    if (at < n) {
-      const int4 *p = reinterpret_cast<const int4 *>(a.plan + a.p.units() + (int64_t)AttnPlan::kUnit * (at / (uint32_t)a.s.Hkv));
-      r0 = p[0];
-      r1 = p[1];
-    }
-  }
-  // False at the end. Call done() after each item.
-  __device__ __forceinline__ bool item(Item &it) {
-    if (at >= n) return false;
-    it.u = AttnUnit{r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-    it.head = (int)(at % (uint32_t)a.s.Hkv);
-    it.blocks = it.u.kb1 - it.u.kb0;
-    it.pair = it.u.tokens > a.s.tile_tokens;
-    ++k;
-    fetch();
-    return true;
-  }
-  __device__ __forceinline__ void done(const Item &it) {
-    pos += it.blocks;
-    ++index;
-  }
-  // Stream t's blocks of the item: from first(t) on, every step(it)-th one.
-  __device__ __forceinline__ int first(const Item &it, int t) const { return it.pair ? 0 : (int)((pos ^ (uint32_t)t) & 1u); }
-  __device__ __forceinline__ int step(const Item &it) const { return it.pair ? 1 : 2; }
-};
-
-// Keys that every row of a unit sees.
-__device__ __forceinline__ int common_keys(const AttnUnit &u, int causal) { return visible_keys(u.pos0, u.kv_len, causal); }
 
 // ------------------------------------------------------------------ kernel
 
@@ -422,8 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         w.done(it);
       }
     } else {
-      // ---- values that not every row sees: each warp looks at every kFixWarps-th group of 32 chunks of 16 bytes
-      constexpr int kChunks = D / 8;  // of a row
+      // ---- values that not every row sees
       const int me = (warp - kFixWarp) * 32 + lane;
       uint32_t slot = 0, phase = 0;
       bool ok = true;
@@ -433,33 +285,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           const int j0 = (it.u.kb0 + b) * kKeyBlock;
           if (!await(&vfull[slot], phase, a.err, kErrAttn)) { ok = false; break; }
           if (j0 + kKeyBlock > seen) {
-            unsigned char *base = sm + S::kVOff + slot * S::kTileBytes;
-            auto chunk = [&](int i) {
-              const int r = i / kChunks, c = i % kChunks;
-              return reinterpret_cast<uint4 *>(base + (c / 8) * S::kHalfBytes + swz128(r, c % 8));
-            };
-            const int i0 = max(0, seen - j0) * kChunks, i1 = min(kKeyBlock, it.u.kv_len - j0) * kChunks;  // looked at; zeroed from i1 on
-            uint32_t any = 0;  // an exponent of all ones, plus one, carries into its sign
-#pragma unroll 4
-            for (int i = i0 + me; i < i1; i += 32 * kFixWarps) {
-              const uint4 x = *chunk(i);
-              any |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
-                     ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
-            }
-            if (any & 0x80008000u) {
-              flags[w.index % kFlags] = (int)w.index;
-              for (int i = i0 + me; i < i1; i += 32 * kFixWarps) {
-                const uint4 x = *chunk(i);
-                uint32_t q[4] = {x.x, x.y, x.z, x.w};
+            const int r1 = min(kKeyBlock, it.u.kv_len - j0);
+            unsigned char *block = sm + S::kVOff + slot * S::kTileBytes;
+            if (fix_values<D>(block, S::kHalfBytes, max(0, seen - j0), r1, me, 32 * kFixWarps)) flags[w.index % kFlags] = (int)w.index;
+            for (int i = ((r1 + 15) & ~15) * 128 + 16 * me; i < kKeyBlock * 128; i += 512 * kFixWarps)  // the MMA takes all 128 rows
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if ((q[e] & 0x7f80u) == 0x7f80u) q[e] &= 0xffff0000u;
-                  if ((q[e] & 0x7f800000u) == 0x7f800000u) q[e] &= 0xffffu;
-                }
-                *chunk(i) = make_uint4(q[0], q[1], q[2], q[3]);
-              }
-            }
-            for (int i = i1 + me; i < kKeyBlock * kChunks; i += 32 * kFixWarps) *chunk(i) = make_uint4(0, 0, 0, 0);
+              for (int h = 0; h < S::kHalves; ++h) *reinterpret_cast<uint4 *>(block + h * S::kHalfBytes + i) = make_uint4(0, 0, 0, 0);
             fence_async_smem();
           }
           __syncwarp();
@@ -692,33 +523,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
 }
 
 // ------------------------------------------------------------------ host side
-
-cudaError_t encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-                   const cuuint32_t *box) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
-  if (enc == nullptr) return cudaErrorNotSupported;
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, es,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-// Rows of `heads` heads of D elements, boxes of 64 elements x box_heads x box_rows.
-cudaError_t encode_rows(CUtensorMap *m, const void *base, int D, int heads, int64_t head, int64_t rows, int64_t ld, int box_heads,
-                        int box_rows) {
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
-  const cuuint64_t strides[2] = {(cuuint64_t)head * 2, (cuuint64_t)ld * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
-  return encode(m, base, 3, dims, strides, box);
-}
-
-cudaError_t encode_pages(CUtensorMap *m, const void *base, const AttnArgs &a, int64_t row, int64_t head, int64_t page) {
-  const cuuint64_t dims[4] = {(cuuint64_t)a.s.D, (cuuint64_t)a.kv.page_size, (cuuint64_t)a.s.Hkv, (cuuint64_t)a.kv.num_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)row * 2, (cuuint64_t)head * 2, (cuuint64_t)page * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)std::min(a.kv.page_size, kKeyBlock), 1, 1};
-  return encode(m, base, 4, dims, strides, box);
-}
 
 template <int D, bool PAGED>
 cudaError_t launch(const AttnArgs &a, cudaStream_t st) {
