@@ -24,6 +24,8 @@ struct AttnShape {
   int slot_rows;     // rows of a partial result
   int ctas;          // CTAs the work is cut for
   int min_cost;      // least cost of a piece of a split unit
+  float piece_cost, join_cost;  // what a piece, and joining, take besides
+  float alone;       // time of a piece that runs when few others do
   int max_slots;     // partial results of one key-value head, at most
   float scale_log2;  // score scale times log2(e)
 };

@@ -3,10 +3,13 @@
 //
 // Plan: a sequence's rows are cut into units (up to two 128-row tiles of one
 // key-value head's query heads), a unit's cost is its blocks of keys times its
-// tiles. A unit above the even share of a CTA, total cost x heads / CTAs, is cut
-// along its keys; the units are written in the order of falling cost, so that
-// CTAs that take every ctas-th one end together. One CTA does it all; it is
-// latency: 256 sequences of one row 6 us, and a step pays it once for all layers.
+// tiles. Units above a size are cut along their keys; the units are written in the
+// order of falling cost, so that CTAs that take every ctas-th one end together. The
+// size is the even share of a CTA, total cost x heads / CTAs, where there are many
+// units; where there are few, 32 sizes around it are tried, a warp each, and the one
+// is taken whose rounds of CTAs end first (three sequences of 110 thousand keys: 168
+// pieces of a share on 152 CTAs 299 us, 144 larger ones TODO us). One CTA does it
+// all; it is latency, which a step pays once for all layers.
 //
 // Cache write: a warp a row, all of its 16-byte loads in flight before the first
 // store; it moves each byte once in and once out.
@@ -40,6 +43,11 @@ AttnShape attn_shape(const lora_seqs &q) {
   }
   s.ctas = (s.tc ? 1 : 2) * std::max(1, sm_count());
   s.min_cost = 2;
+  // In blocks of keys by tiles, as measured: units of few rows take 1.5 us a block while all CTAs read, 0.86 us alone;
+  // one of two tiles takes 0.85 us a tile, whatever the others do.
+  s.alone = s.few > 0 ? 0.57f : 1.f;
+  s.piece_cost = s.few > 0 ? 1.f : 5.f;
+  s.join_cost = s.few > 0 ? 2.5f : 8.f;
   s.max_slots = 2 * s.ctas / s.Hkv + 2;
   s.scale_log2 = (float)((double)q.scale * 1.4426950408889634);
   return s;
@@ -74,6 +82,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kBins = 256;
+constexpr int kNear = 1024;  // sequences that are kept in shared memory
 
 struct PlanArgs {
   AttnShape s;
@@ -157,10 +166,16 @@ __device__ __forceinline__ Cut cut_of(const PlanArgs &a, const int32_t *cum, con
 
 __global__ void __launch_bounds__(kThreads) prepare_seqs_kernel(const PlanArgs a) {
   __shared__ unsigned long long part[32], total_cost;
-  __shared__ int bins[kBins], maxima[kThreads / 32], bad, most, groups;
+  __shared__ int bins[kBins], maxima[kThreads / 32], bad, most, groups, sizes[kThreads / 32], costs[kThreads];
+  __shared__ float ends[kThreads / 32];
+  __shared__ int4 near_seqs[kNear];
+  __shared__ int32_t near_cum[kNear];
   const int tid = threadIdx.x;
-  int32_t *cum = a.plan + a.p.cum();
-  int4 *seqs = reinterpret_cast<int4 *>(a.plan + a.p.seqs());
+  int32_t *const out_cum = a.plan + a.p.cum();
+  int4 *const out_seqs = reinterpret_cast<int4 *>(a.plan + a.p.seqs());
+  const bool near = a.S <= kNear;
+  int32_t *cum = near ? near_cum : out_cum;
+  int4 *seqs = near ? near_seqs : out_seqs;
   if (tid == 0) {
     total_cost = 0;
     bad = most = groups = 0;
@@ -181,6 +196,7 @@ __global__ void __launch_bounds__(kThreads) prepare_seqs_kernel(const PlanArgs a
       const bool good = r0 >= 0 && r1 >= r0 && r1 <= a.T && kv >= 0 && kv <= a.max_kv;
       if (!good) atomicAdd(&bad, 1);
       seqs[b] = good ? make_int4(r0, r1 - r0, kv, 0) : make_int4(0, 0, 0, 0);
+      if (near) out_seqs[b] = seqs[b];
       u = good ? (r1 - r0 + a.s.unit_tokens - 1) / a.s.unit_tokens : 0;
       row = good ? r0 : 0;
     }
@@ -202,16 +218,54 @@ __global__ void __launch_bounds__(kThreads) prepare_seqs_kernel(const PlanArgs a
   __syncthreads();
   unsigned long long mine = 0;
   int top = 0;
+  Cut own{};  // this thread's unit, where there is at most one
   for (int i = tid; i < n; i += kThreads) {
-    const Cut c = cut_of(a, cum, seqs, i);
-    mine += c.cost;
-    top = max(top, c.cost);
+    own = cut_of(a, cum, seqs, i);
+    mine += own.cost;
+    top = max(top, own.cost);
   }
-  if (mine > 0) atomicAdd(&total_cost, mine);
-  if (top > 0) atomicMax(&most, top);
+  costs[tid] = own.cost;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((tid & 31) == 0 && mine > 0) {
+    atomicAdd(&total_cost, mine);
+    atomicMax(&most, top);
+  }
   __syncthreads();
   const int64_t share = ((int64_t)total_cost * a.s.Hkv + a.s.ctas - 1) / a.s.ctas;
-  const int64_t chunk = max((int64_t)a.s.min_cost, share);
+  int64_t chunk = max((int64_t)a.s.min_cost, share) * 5 / 4;  // units above it are cut
+  int64_t piece = max((int64_t)a.s.min_cost, share);          // into pieces of about this cost
+  if (n <= kThreads && (int64_t)n * a.s.Hkv <= 2 * a.s.ctas) {
+    // Sizes from half a share to 2.4 shares, and no cut at all. The last CTA ends with the largest piece, or where the
+    // share and the smallest piece on top of it end, or, of even pieces, with a whole round; pieces that are left over
+    // run faster where the others' traffic was the limit. A piece's beginning and end and the joining cost blocks' time too.
+    const int warp = tid >> 5, lane = tid & 31;
+    const int size = warp == 31 ? INT32_MAX / 2 : (int)max((int64_t)a.s.min_cost, share * (8 + warp) / 16 + 1);
+    int pieces = 0, largest = 0, smallest = INT32_MAX;
+    for (int i = lane; i < n; i += 32) {
+      const int p = max(1, (costs[i] + size - 1) / size), each = (costs[i] + p - 1) / p;
+      pieces += p;
+      largest = max(largest, each);
+      smallest = min(smallest, each);
+    }
+    pieces = __reduce_add_sync(0xffffffffu, pieces);
+    largest = __reduce_max_sync(0xffffffffu, largest);
+    smallest = __reduce_min_sync(0xffffffffu, smallest);
+    if (lane == 0) {
+      const int items = pieces * a.s.Hkv, rounds = (items + a.s.ctas - 1) / a.s.ctas, last = items - (rounds - 1) * a.s.ctas;
+      const float average = (float)total_cost / (float)max(1, pieces);
+      const float even = ((float)(rounds - 1) + (2 * last > a.s.ctas ? 1.f : a.s.alone)) * average;
+      const float end = fmaxf((float)largest * a.s.alone, fminf(even, (float)share + (float)smallest));
+      ends[warp] = pieces - n > a.s.max_slots / 2 ? INFINITY : end + a.s.piece_cost * (float)rounds + (pieces > n ? a.s.join_cost : 0.f);
+      sizes[warp] = size;
+    }
+    __syncthreads();
+    int best = 31;
+    for (int x = 30; x >= 0; --x)
+      if (ends[x] < ends[best]) best = x;
+    chunk = piece = sizes[best];
+  }
   const int peak = max(1, most);
   auto bin_of = [&](int cost) { return kBins - 1 - (int)((int64_t)cost * (kBins - 1) / peak); };
   // Twice over the units: the pieces of each cost counted, then written in that order.
@@ -222,8 +276,8 @@ __global__ void __launch_bounds__(kThreads) prepare_seqs_kernel(const PlanArgs a
       Cut c{};
       int pieces = 0;
       if (i < n) {
-        c = cut_of(a, cum, seqs, i);
-        pieces = c.cost > chunk + chunk / 4 ? (int)min((int64_t)c.blocks, (c.cost + chunk - 1) / chunk) : 1;
+        c = n <= kThreads ? own : cut_of(a, cum, seqs, i);
+        pieces = c.cost > chunk ? (int)min((int64_t)c.blocks, (c.cost + piece - 1) / piece) : 1;
       }
       const bool wants = pieces > 1;
       const unsigned long long at = base + block_scan(wants ? (unsigned long long)pieces : 0ull, part, &total);

@@ -197,36 +197,65 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const Att
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int steps = (a.s.slot_rows + kJoinWarps - 1) / kJoinWarps;
-  const int n = a.plan[AttnPlan::kGroups] * a.s.Hkv * steps;
   const int64_t pitch = slot_floats(a.s) * a.s.Hkv;  // from one piece to the next
+  // The first group's record is asked for with the number of groups, a row's first outputs with its statistics: three
+  // round trips to memory instead of five.
+  auto group_at = [&](int i) {
+    return *reinterpret_cast<const int4 *>(a.plan + a.p.groups() +
+                                           (int64_t)AttnPlan::kGroup * min(i / steps / a.s.Hkv, a.p.max_groups - 1));
+  };
+  int4 g = group_at(blockIdx.x);
+  const int n = a.plan[AttnPlan::kGroups] * a.s.Hkv * steps;
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    if (i != blockIdx.x) g = group_at(i);
     const int step = i % steps, head = i / steps % a.s.Hkv;
-    const int4 g = *reinterpret_cast<const int4 *>(a.plan + a.p.groups() + (int64_t)AttnPlan::kGroup * (i / steps / a.s.Hkv));
     const int row = step * kJoinWarps + warp;
     if (row >= g.y * a.s.G) continue;
     const float *part = a.ws + ((int64_t)g.z * a.s.Hkv + head) * slot_floats(a.s);
     const float *stats = part + (int64_t)a.s.slot_rows * a.s.D + 2 * row;
-    float m = -INFINITY;
-    for (int j = lane; j < g.w; j += 32) m = fmaxf(m, stats[j * pitch]);
+    const float *first = part + (int64_t)row * a.s.D + lane;
+    constexpr int kAhead = 4;  // pieces whose first 128 elements are in flight with the statistics
+    float ahead[kAhead][4];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ahead[k][e] = k < g.w && 32 * e + lane < a.s.D ? first[k * pitch + 32 * e] : 0.f;
+    float2 mine = lane < g.w ? *reinterpret_cast<const float2 *>(stats + lane * pitch) : make_float2(-INFINITY, 0.f);
+    float m = mine.x;
+    for (int j = lane + 32; j < g.w; j += 32) m = fmaxf(m, stats[j * pitch]);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
     const float base = m == -INFINITY ? 0.f : m;
     float acc[8] = {}, l = 0.f;
     for (int j0 = 0; j0 < g.w; j0 += 32) {
       const int j = j0 + lane;
-      const float w = j < g.w ? exp2f(stats[j * pitch] - base) : 0.f;
-      float lw = j < g.w ? w * stats[j * pitch + 1] : 0.f;
+      if (j0 > 0) mine = j < g.w ? *reinterpret_cast<const float2 *>(stats + j * pitch) : make_float2(-INFINITY, 0.f);
+      const float w = exp2f(mine.x - base);
+      float lw = w * mine.y;
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, x);
       l += lw;
       const int here = min(32, g.w - j0);
+      if (j0 == 0) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, k);
+          if (k < here) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = fmaf(wk, ahead[k][e], acc[e]);
+#pragma unroll
+            for (int e = 4; e < 8; ++e)
+              if (32 * e + lane < a.s.D) acc[e] = fmaf(wk, first[k * pitch + 32 * e], acc[e]);
+          }
+        }
+      }
 #pragma unroll 4
-      for (int k = 0; k < here; ++k) {
+      for (int k = j0 == 0 ? kAhead : 0; k < here; ++k) {
         const float wk = __shfl_sync(0xffffffffu, w, k);
-        const float *o = part + (j0 + k) * pitch + (int64_t)row * a.s.D;
+        const float *o = first + (j0 + k) * pitch;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (32 * e + lane < a.s.D) acc[e] = fmaf(wk, o[32 * e + lane], acc[e]);
+          if (32 * e + lane < a.s.D) acc[e] = fmaf(wk, o[32 * e], acc[e]);
       }
     }
     const int64_t t = g.x + row / a.s.G;

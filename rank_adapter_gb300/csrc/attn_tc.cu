@@ -192,7 +192,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         for (int b = b0; b < it.blocks; b += d, ++steps) {
           const uint32_t pos = w.pos + b, slot = pos % S::kV;
           const uint64_t vd_now = vd + slot * (S::kTileBytes >> 4);
-          if (!(ok = operands() && await(&fixed[slot], pos / S::kV & 1, a.err, kErrAttn) &&
+          // The next step's operands are asked for ahead of this one's weights, but where they are another unit's: its Q
+          // is loaded only now, and this unit's last product must not wait for it.
+          const bool ahead = sb < is.blocks;
+          if (!(ok = (!ahead || operands()) && await(&fixed[slot], pos / S::kV & 1, a.err, kErrAttn) &&
                      await(&pfull[2 * t], steps & 1, a.err, kErrAttn)))
             break;
           // Streams of two tiles take turns: left alone they fall into step, and the tensor core idles while both take
@@ -204,10 +207,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           tc_after_sync();
           mma_pv4(to, ts + 32, vd_now + (64 * 128 >> 4), 128, id_o, 1);
           if (b + d >= it.blocks) mma_commit_elect(&ofull[t]);
-          if (more) scores();
+          if (ahead) scores();
           if (it.pair && lane == 0) mbar_arrive(&go[t ^ 1]);
           mma_commit_elect(&vfree[slot]);
           if (!it.pair) mma_commit_elect(&vfree[slot]);
+          if (!ahead) {
+            if (!(ok = operands())) break;
+            if (more) scores();
+          }
           if (more) scores_done();
         }
         w.done(it);
@@ -275,7 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         w.done(it);
       }
     } else {
-      // ---- values that not every row sees
+      // ---- values that not every row sees: each warp looks at every kFixWarps-th group of 32 chunks of 16 bytes
+      constexpr int kChunks = D / 8;  // of a row
       const int me = (warp - kFixWarp) * 32 + lane;
       uint32_t slot = 0, phase = 0;
       bool ok = true;
@@ -285,12 +293,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           const int j0 = (it.u.kb0 + b) * kKeyBlock;
           if (!await(&vfull[slot], phase, a.err, kErrAttn)) { ok = false; break; }
           if (j0 + kKeyBlock > seen) {
-            const int r1 = min(kKeyBlock, it.u.kv_len - j0);
-            unsigned char *block = sm + S::kVOff + slot * S::kTileBytes;
-            if (fix_values<D>(block, S::kHalfBytes, max(0, seen - j0), r1, me, 32 * kFixWarps)) flags[w.index % kFlags] = (int)w.index;
-            for (int i = ((r1 + 15) & ~15) * 128 + 16 * me; i < kKeyBlock * 128; i += 512 * kFixWarps)  // the MMA takes all 128 rows
+            unsigned char *base = sm + S::kVOff + slot * S::kTileBytes;
+            auto chunk = [&](int i) {
+              const int r = i / kChunks, c = i % kChunks;
+              return reinterpret_cast<uint4 *>(base + (c / 8) * S::kHalfBytes + swz128(r, c % 8));
+            };
+            const int i0 = max(0, seen - j0) * kChunks, i1 = min(kKeyBlock, it.u.kv_len - j0) * kChunks;  // looked at; zeroed from i1 on
+            uint32_t any = 0;  // an exponent of all ones, plus one, carries into its sign
+#pragma unroll 4
+            for (int i = i0 + me; i < i1; i += 32 * kFixWarps) {
+              const uint4 x = *chunk(i);
+              any |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                     ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+            }
+            if (any & 0x80008000u) {
+              flags[w.index % kFlags] = (int)w.index;
+              for (int i = i0 + me; i < i1; i += 32 * kFixWarps) {
+                const uint4 x = *chunk(i);
+                uint32_t q[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-              for (int h = 0; h < S::kHalves; ++h) *reinterpret_cast<uint4 *>(block + h * S::kHalfBytes + i) = make_uint4(0, 0, 0, 0);
+                for (int e = 0; e < 4; ++e) {
+                  if ((q[e] & 0x7f80u) == 0x7f80u) q[e] &= 0xffff0000u;
+                  if ((q[e] & 0x7f800000u) == 0x7f800000u) q[e] &= 0xffffu;
+                }
+                *chunk(i) = make_uint4(q[0], q[1], q[2], q[3]);
+              }
+            }
+            for (int i = i1 + me; i < kKeyBlock * kChunks; i += 32 * kFixWarps) *chunk(i) = make_uint4(0, 0, 0, 0);
             fence_async_smem();
           }
           __syncwarp();
