@@ -93,7 +93,7 @@ int run(const lora_seqs *s, ra::AttnArgs &a, const void *q, int64_t ldq, void *o
   a.num_tokens = s->num_tokens;
   const int64_t max_kv = has_cache(s) ? (int64_t)s->page_size * s->max_pages : s->num_tokens;
   const cudaStream_t st_ = (cudaStream_t)stream;
-  cudaError_t e = a.s.few > 0 && a.kv.page_size > 0 ? ra::launch_attn_few(a, st_)
+  cudaError_t e = a.s.few > 0 ? ra::launch_attn_few(a, st_)
                   : a.s.tc                          ? ra::launch_attn_tc(a, st_)
                                                     : ra::launch_attn_rows(a, st_);
   if (e == cudaSuccess && ra::attn_may_split(a.s, max_kv)) e = ra::launch_attn_combine(a, (cudaStream_t)stream);

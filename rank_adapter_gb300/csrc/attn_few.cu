@@ -1,13 +1,14 @@
-// Attention of few rows over a paged cache on the tensor cores (bf16, heads of 128): the
-// single tokens and short drafts of a decode step, whose time is that of reading the
-// cache.
+// Attention of few rows on the tensor cores (bf16, heads of 64 and 128): the single tokens
+// and short drafts of a decode step, whose time is that of reading the cache, and small
+// batches, whose time is that of one pass from end to end.
 //
 // The keys take the MMA's long side and a unit's N = 16, 32 or 64 rows (token, query head)
 // its short one, so that little is computed for rows that are not there, and shared memory
 // goes to blocks in flight (3 of K and 3 or 2 of V, 160 to 192 KB):
 //   S^T = K Q^T     128 keys by N, in TMEM, a thread a key
 //   P^T = 2^(c S^T - m)    bf16, to shared memory, a thread its key's N weights
-//   O^T += V^T P^T  128 elements of the head by N, in TMEM, a thread an element
+//   O^T += V^T P^T  128 elements of the head by N, in TMEM, a thread an element (a head of
+//                   64 leaves the other 64 rows to whatever lies behind the block)
 // The base m of a row is common to its keys. It need not be their largest score: fp32 and
 // bf16 carry a common factor of 2^24 without loss. A unit begins with the score of its
 // first key, and the base rises to the largest score so far where the threads agree (one
@@ -26,12 +27,12 @@ constexpr float kLazy = 24.f;     // log2 of the factor that a weight may exceed
 constexpr float kLowest = -3e38f; // base of a row without a key so far
 constexpr int kFlags = 8;         // units that the loads can be ahead of an epilogue, and more
 
-template <int N_>
+template <int N_, int D_>
 struct FewShape {
-  static constexpr int N = N_, D = 128;
-  static constexpr int kHalfBytes = kKeys * 128, kTileBytes = 2 * kHalfBytes;  // a K or V block: 64 elements of 128 keys, twice
-  static constexpr uint32_t kK = 3, kV = N == 64 ? 2 : 3, kQ = 2, kP = N == 64 ? 1 : 2;
-  static constexpr int kQHalf = N * 128, kQBytes = 2 * kQHalf, kPBytes = kKeys * N * 2;
+  static constexpr int N = N_, D = D_, kHalves = D / 64;
+  static constexpr int kHalfBytes = kKeys * 128, kTileBytes = kHalves * kHalfBytes;  // a K or V block, 64 elements at a time
+  static constexpr uint32_t kK = D == 64 ? 6 : 3, kV = D == 64 ? 5 : N == 64 ? 2 : 3, kQ = 2, kP = N == 64 ? 1 : 2;
+  static constexpr int kQHalf = N * 128, kQBytes = kHalves * kQHalf, kPBytes = kKeys * N * 2;
   static constexpr uint32_t kPLayout = N == 16 ? kSw32 : N == 32 ? kSw64 : kSw128;
   static constexpr int kKOff = 0, kVOff = kKOff + (int)kK * kTileBytes, kQOff = kVOff + (int)kV * kTileBytes;
   static constexpr int kPOff = kQOff + (int)kQ * kQBytes;
@@ -39,14 +40,16 @@ struct FewShape {
   static constexpr int kWarpOff = kRowOff + N * 20 + 16 - N * 20 % 16;  // a value of each row from each warp
   static constexpr int kBarOff = kWarpOff + 4 * N * 4;
   static constexpr int kBarriers = 2 * (int)kK + 3 * (int)kV + 2 * (int)kQ + 2 + 2 * (int)kP + 1;
-  static constexpr int kSmem = 1024 + kBarOff + kBarriers * 8 + 16 + kFlags * 4;
+  static constexpr int kWalkOff = kBarOff + (kBarriers * 8 + 16 + kFlags * 4 + 15) / 16 * 16;
+  static constexpr int kEnd = kWalkOff + 32 * (kThreads / 32 + 1);
+  static constexpr int kSmem = 1024 + (kEnd > kQOff + kHalfBytes ? kEnd : kQOff + kHalfBytes);  // what the MMA reads behind V, too
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static constexpr uint32_t kO = 2 * N, kTmemCols = N == 16 ? 64 : N == 32 ? 128 : 256;  // TMEM: two S, then O
 };
 
 struct FewMaps {
   CUtensorMap q;     // {D, heads, rows}, boxes of 64 x group x unit tokens
-  CUtensorMap k, v;  // {D, keys of a page, heads, pages}, boxes of 64 x keys x 1 x 1
+  CUtensorMap k, v;  // pages: {D, keys of a page, heads, pages}, boxes of 64 x keys x 1 x 1; packed rows: {D, heads, rows}, 64 x 1 x 128
 };
 
 // Barrier of the four softmax warps; the second one says whether any thread's p holds.
@@ -83,10 +86,9 @@ __device__ __forceinline__ void store_across(float *to, const float (&v)[N], int
   }
 }
 
-template <int N>
+template <int N, int D, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_constant__ FewMaps maps, const AttnArgs a) {
-  using S = FewShape<N>;
-  constexpr int D = S::D;
+  using S = FewShape<N, D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *sm = align1024(smem_raw);
   uint64_t *kfull = reinterpret_cast<uint64_t *>(sm + S::kBarOff);  // a K block is in
@@ -144,16 +146,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
   tc_after_sync();
   pdl_trigger();  // only now: a successor that takes TMEM must not start before this CTA has its own
   const uint32_t tmem = *tslot;
-  Walk w(a);
+  Walk w(a, sm + S::kWalkOff + 32 * warp);
   Item it;
 
   if (warp == kMmaWarp) {
     // ---- MMA issue
-    constexpr uint32_t id_s = idesc_kk(kKeys, N), id_o = idesc_bf16(D, N) | (1u << 15);  // both operands as they lie
+    constexpr uint32_t id_s = idesc_kk(kKeys, N), id_o = idesc_bf16(128, N) | (1u << 15);  // both operands as they lie
     const uint64_t kd = smem_desc(smem_addr(sm + S::kKOff), 16, 1024, kSw128), qd = smem_desc(smem_addr(sm + S::kQOff), 16, 1024, kSw128);
+    // (With one half, the MMA's other 64 rows come from the next block or from Q, and go nowhere.)
     const uint64_t vd = smem_desc(smem_addr(sm + S::kVOff), S::kHalfBytes, 1024, kSw128);
     const uint64_t pd = smem_desc(smem_addr(sm + S::kPOff), 16, 16 * N, S::kPLayout);
-    Walk ws(a);      // of the scores, a block ahead
+    Walk ws(a, sm + S::kWalkOff + kThreads);  // of the scores, a block ahead
     Item is{};
     int sb = 0;
     bool more = ws.item(is);
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
       const uint32_t slot = gs % S::kK, qs = (items - 1) % S::kQ;
       if (!await(&kfull[slot], gs / S::kK & 1, a.err, kErrAttn)) return false;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < S::kHalves; ++h)
         mma_run<4>(tmem + (gs & 1) * N, kd + slot * (S::kTileBytes >> 4) + h * (S::kHalfBytes >> 4),
                    qd + qs * (S::kQBytes >> 4) + h * (S::kQHalf >> 4), 2, 2, id_s, h > 0);
       mma_commit_elect(&sfull[gs & 1]);
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
     uint64_t *full = keys ? kfull : vfull, *free = keys ? kfree : vfree;
     const CUtensorMap *map = keys ? &maps.k : &maps.v;
     unsigned char *ring = sm + (keys ? S::kKOff : S::kVOff);
-    const int half = lane & 1, part = lane >> 1, ps = a.kv.page_size, rows = min(ps, kKeyBlock);
+    const int half = lane % S::kHalves, part = lane / S::kHalves, ps = PAGED ? a.kv.page_size : kKeyBlock, rows = min(ps, kKeyBlock);
     const uint32_t n_slots = keys ? S::kK : S::kV;
     uint32_t slot = 0, phase = 0, items = 0;
     bool ok = true;
@@ -218,15 +221,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
         const uint32_t qs = items % S::kQ;
         if (!await(&qfree[qs], (items / S::kQ & 1) ^ 1, a.err, kErrAttn)) break;
         ++items;
-        if (lane == 0) mbar_arrive_tx(&qfull[qs], (uint32_t)(2 * a.s.unit_tokens * a.s.G * 128));
+        if (lane == 0) mbar_arrive_tx(&qfull[qs], (uint32_t)(S::kHalves * a.s.unit_tokens * a.s.G * 128));
         __syncwarp();
-        if (lane < 2)
+        if (lane < S::kHalves)
           tma_load_3d(sm + S::kQOff + qs * S::kQBytes + lane * S::kQHalf, &maps.q, lane * 64, it.head * a.s.G, it.u.row0, &qfull[qs]);
       }
       const int32_t *table = a.kv.table + (int64_t)it.u.seq * a.kv.ld_table;
       auto page_at = [&](int b) {  // a lane a page of block b: its id, or one past the cache (which reads zeros)
         const int j = (it.u.kb0 + b) * kKeyBlock + part * rows;
         int page = 0;
+        if (!PAGED) return page;
         if (b < it.blocks && part * rows < kKeyBlock && j < it.u.kv_len) {
           page = table[j >> a.kv.log2_page];
           if ((unsigned)page >= (unsigned)a.kv.num_pages) {
@@ -240,13 +244,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
       for (int b = 0; b < it.blocks; ++b) {
         const int page = next, j0 = (it.u.kb0 + b) * kKeyBlock;
         next = page_at(b + 1);
-        const int copies = (min(kKeyBlock, it.u.kv_len - j0) + rows - 1) / rows * 2;
+        const int copies = PAGED ? (min(kKeyBlock, it.u.kv_len - j0) + rows - 1) / rows * S::kHalves : S::kHalves;
         if (!await(&free[slot], phase ^ 1, a.err, kErrAttn)) { ok = false; break; }
         if (lane == 0) mbar_arrive_tx(&full[slot], (uint32_t)(copies * rows * 128));
         __syncwarp();
-        if (lane < copies)
-          tma_load_4d(ring + slot * S::kTileBytes + half * S::kHalfBytes + part * rows * 128, map, half * 64,
-                      (j0 + part * rows) & (ps - 1), it.head, page, &full[slot]);
+        if (lane < copies) {
+          unsigned char *dst = ring + slot * S::kTileBytes + half * S::kHalfBytes + part * rows * 128;
+          if constexpr (PAGED) tma_load_4d(dst, map, half * 64, (j0 + part * rows) & (ps - 1), it.head, page, &full[slot]);
+          else tma_load_3d(dst, map, half * 64, it.head, it.u.row0 - it.u.pos0 + j0, &full[slot]);
+        }
         if (++slot == n_slots) {
           slot = 0;
           phase ^= 1;
@@ -411,27 +417,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
         for (int y = 0; y < 16; ++y) {
           const int64_t at = to_row[x + y];
           const float v = some ? o[y] * factor[x + y] : 0.f;
-          if (at < 0) continue;
+          if (at < 0 || tid >= D) continue;
           if (split) *reinterpret_cast<float *>(to + at) = v;
           else *reinterpret_cast<__nv_bfloat16 *>(to + at) = __float2bfloat16_rn(v);
         }
       }
       tc_before_sync();
       if (some && flags[w.index % kFlags] == (int)w.index) {
-        // Values that were taken out, for the rows that see them: next to one, what is finite does not count.
-        for (int n = 0; n < rows; ++n) {
-          const int end = min(sees[n], it.u.kb1 * kKeyBlock);
-          float sum = 0.f;
-          for (int j = max(seen, it.u.kb0 * kKeyBlock); j < end; ++j) {
-            const int page = a.kv.table[(int64_t)it.u.seq * a.kv.ld_table + (j >> a.kv.log2_page)];
-            if ((unsigned)page >= (unsigned)a.kv.num_pages) continue;
-            const float f = __bfloat162float(static_cast<const __nv_bfloat16 *>(
-                a.kv.v)[page * a.kv.v_page + (j & (a.kv.page_size - 1)) * a.kv.v_row + it.head * a.kv.v_head + tid]);
-            if (!isfinite(f)) sum += f;
-          }
+        // Values that were taken out, for the rows that see them.
+        for (int n = 0; n < rows && tid < D; ++n) {
+          const float sum = taken_out(a, it.u, it.head, tid, seen, sees[n]);
           if (sum == 0.f) continue;
-          if (split) *reinterpret_cast<float *>(to + to_row[n]) += sum;
-          else {
+          if (split) {
+            *reinterpret_cast<float *>(to + to_row[n]) += sum;
+          } else {
             __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(to + to_row[n]);
             *p = __float2bfloat16_rn(__bfloat162float(*p) + sum);
           }
@@ -448,25 +447,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
   }
 }
 
-template <int N>
+template <int N, int D, bool PAGED>
 cudaError_t launch(const AttnArgs &a, cudaStream_t st) {
   FewMaps maps;
-  cudaError_t e = encode_rows(&maps.q, a.q, a.s.D, a.s.Hq, a.s.D, a.num_tokens, a.ldq, a.s.G, a.s.unit_tokens);
-  if (e == cudaSuccess) e = encode_pages(&maps.k, a.kv.k, a, a.kv.k_row, a.kv.k_head, a.kv.k_page);
-  if (e == cudaSuccess) e = encode_pages(&maps.v, a.kv.v, a, a.kv.v_row, a.kv.v_head, a.kv.v_page);
-  if (e == cudaSuccess) e = set_max_dynamic_smem((const void *)attn_few_kernel<N>, FewShape<N>::kSmem);
+  cudaError_t e = encode_rows(&maps.q, a.q, D, a.s.Hq, D, a.num_tokens, a.ldq, a.s.G, a.s.unit_tokens);
+  if (PAGED) {
+    if (e == cudaSuccess) e = encode_pages(&maps.k, a.kv.k, a, a.kv.k_row, a.kv.k_head, a.kv.k_page);
+    if (e == cudaSuccess) e = encode_pages(&maps.v, a.kv.v, a, a.kv.v_row, a.kv.v_head, a.kv.v_page);
+  } else {
+    if (e == cudaSuccess) e = encode_rows(&maps.k, a.kv.k, D, a.s.Hkv, a.kv.k_head, a.num_tokens, a.kv.k_row, 1, kKeys);
+    if (e == cudaSuccess) e = encode_rows(&maps.v, a.kv.v, D, a.s.Hkv, a.kv.v_head, a.num_tokens, a.kv.v_row, 1, kKeys);
+  }
+  if (e == cudaSuccess) e = set_max_dynamic_smem((const void *)attn_few_kernel<N, D, PAGED>, FewShape<N, D>::kSmem);
   if (e != cudaSuccess) return e;
   const int64_t most = (int64_t)a.p.max_units * a.s.Hkv;
-  return launch_pdl(attn_few_kernel<N>, dim3((unsigned)std::min<int64_t>(most, a.s.ctas)), dim3(kThreads), FewShape<N>::kSmem, st, 1u,
-                    maps, a);
+  return launch_pdl(attn_few_kernel<N, D, PAGED>, dim3((unsigned)std::min<int64_t>(most, a.s.ctas)), dim3(kThreads),
+                    FewShape<N, D>::kSmem, st, 1u, maps, a);
+}
+
+template <int D, bool PAGED>
+cudaError_t launch(const AttnArgs &a, cudaStream_t st) {
+  if (a.s.few == 16) return launch<16, D, PAGED>(a, st);
+  if (a.s.few == 32) return launch<32, D, PAGED>(a, st);
+  return launch<64, D, PAGED>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_few(const AttnArgs &a, cudaStream_t st) {
-  if (a.s.few == 16) return launch<16>(a, st);
-  if (a.s.few == 32) return launch<32>(a, st);
-  return launch<64>(a, st);
+  const bool paged = a.kv.page_size > 0;
+  if (a.s.D == 128) return paged ? launch<128, true>(a, st) : launch<128, false>(a, st);
+  return paged ? launch<64, true>(a, st) : launch<64, false>(a, st);
 }
 
 }  // namespace ra

@@ -1,23 +1,24 @@
 // Attention on the CUDA cores (fp32, and bf16 heads of other sizes than the
 // tensor-core kernel takes), and the joining of partial results for both.
 //
-// A CTA takes a unit of one key-value head: 32 rows at a time, 8 a warp, over
+// A CTA takes a unit of one key-value head: 32 rows at a time, 4 a warp, over
 // tiles of 32 keys that all its rows share in shared memory. A lane is a key for
 // the scores (rows' maxima and sums by shuffles) and an element of the head for
 // the outputs, with the softmax's running maximum and sum in between. What
-// bounds it is shared memory: a key's element is read once for 8 rows' products.
+// bounds it is shared memory, read 16 bytes at a time: a lane's part of a key
+// serves 4 rows' products.
 #include "attn.cuh"
 #include "tcgen05.cuh"
 
 namespace ra {
 namespace {
 
-constexpr int kWarps = 4, kWarpRows = 8, kRows = kWarps * kWarpRows, kKeys = 32;
+constexpr int kWarps = 8, kWarpRows = 4, kRows = kWarps * kWarpRows, kKeys = 32;
 
 template <typename T, int N>  // N: 32-element steps of a head
 struct RowsSmem {
   static constexpr int kD = 32 * N;
-  float k[kKeys][kD + 1], v[kKeys][kD], q[kRows][kD];
+  float k[kKeys][kD + 4], v[kKeys][kD], q[kRows][kD], p[kWarps][kKeys][kWarpRows];
 };
 
 // Keys [j0, j0 + 32) of the unit's sequence and head to shared memory as fp32; zeros past n keys and past the head.
@@ -58,9 +59,9 @@ __device__ __forceinline__ void load_keys(RowsSmem<T, N> &sm, const AttnArgs &a,
       }
     }
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      sm.k[r][c * kVec + e] = k[e];
-      sm.v[r][c * kVec + e] = v[e];
+    for (int e = 0; e < kVec; e += 4) {
+      *reinterpret_cast<float4 *>(&sm.k[r][c * kVec + e]) = make_float4(k[e], k[e + 1], k[e + 2], k[e + 3]);
+      *reinterpret_cast<float4 *>(&sm.v[r][c * kVec + e]) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
     }
   }
 }
@@ -82,13 +83,13 @@ __global__ void __launch_bounds__(32 * kWarps) attn_rows_kernel(const AttnArgs a
     const int rows = u.tokens * a.s.G;
     for (int r0 = 0; r0 < rows; r0 += kRows) {
       __syncthreads();
-      for (int i = threadIdx.x; i < kRows * 32 * N; i += 32 * kWarps) {
-        const int r = i / (32 * N), d = i % (32 * N), row = r0 + r;
-        float x = 0.f;
+      for (int i = threadIdx.x; i < kRows * 4 * N; i += 32 * kWarps) {  // eight elements of a row
+        const int r = i / (4 * N), d = i % (4 * N) * 8, row = r0 + r;
+        float x[8] = {};
         if (row < rows && d < a.s.D)
-          x = Elem<T>::to_f(static_cast<const T *>(a.q)[(int64_t)(u.row0 + row / a.s.G) * a.ldq +
-                                                         (int64_t)(head * a.s.G + row % a.s.G) * a.s.D + d]);
-        sm.q[r][d] = x;
+          load8_f32(static_cast<const T *>(a.q) + (int64_t)(u.row0 + row / a.s.G) * a.ldq +
+                        (int64_t)(head * a.s.G + row % a.s.G) * a.s.D + d, x);
+        store8(&sm.q[r][d], x);
       }
       float m[kWarpRows], l[kWarpRows], o[kWarpRows][N];
       int lim[kWarpRows], first = INT32_MAX, most = 0;
@@ -112,10 +113,13 @@ __global__ void __launch_bounds__(32 * kWarps) attn_rows_kernel(const AttnArgs a
         if (j0 >= most) continue;
         float s[kWarpRows] = {};
 #pragma unroll 4
-        for (int d = 0; d < 32 * N; ++d) {
-          const float k = sm.k[lane][d];
+        for (int d = 0; d < 32 * N; d += 4) {
+          const float4 k = *reinterpret_cast<const float4 *>(&sm.k[lane][d]);
 #pragma unroll
-          for (int r = 0; r < kWarpRows; ++r) s[r] = fmaf(sm.q[warp * kWarpRows + r][d], k, s[r]);
+          for (int r = 0; r < kWarpRows; ++r) {
+            const float4 q = *reinterpret_cast<const float4 *>(&sm.q[warp * kWarpRows + r][d]);
+            s[r] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[r]))));
+          }
         }
 #pragma unroll
         for (int r = 0; r < kWarpRows; ++r) {
@@ -135,26 +139,29 @@ __global__ void __launch_bounds__(32 * kWarps) attn_rows_kernel(const AttnArgs a
 #pragma unroll
           for (int i = 0; i < N; ++i) o[r][i] *= old;
         }
+        *reinterpret_cast<float4 *>(sm.p[warp][lane]) = make_float4(s[0], s[1], s[2], s[3]);
+        __syncwarp();
         // Rows that do not see key j0 + j take nothing of it, whatever its value.
+#pragma unroll 4
         for (int j = 0; j < kKeys; ++j) {
           if (j0 + j >= most) break;
+          const float4 p4 = *reinterpret_cast<const float4 *>(sm.p[warp][j]);
+          const float p[kWarpRows] = {p4.x, p4.y, p4.z, p4.w};
           float v[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) v[i] = sm.v[j][32 * i + lane];
           if (j0 + j < first) {
 #pragma unroll
             for (int r = 0; r < kWarpRows; ++r) {
-              const float p = __shfl_sync(0xffffffffu, s[r], j);
 #pragma unroll
-              for (int i = 0; i < N; ++i) o[r][i] = fmaf(p, v[i], o[r][i]);
+              for (int i = 0; i < N; ++i) o[r][i] = fmaf(p[r], v[i], o[r][i]);
             }
           } else {
 #pragma unroll
             for (int r = 0; r < kWarpRows; ++r) {
-              const float p = __shfl_sync(0xffffffffu, s[r], j);
               if (j0 + j < lim[r]) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) o[r][i] = fmaf(p, v[i], o[r][i]);
+                for (int i = 0; i < N; ++i) o[r][i] = fmaf(p[r], v[i], o[r][i]);
               }
             }
           }

@@ -52,7 +52,8 @@ struct TcShape {
   static constexpr int kStatOff = kTurnOff + 8 * kTurnBytes;  // {m, l} of a merged stream's rows
   static constexpr int kBarOff = kStatOff + kRows * 8;
   static constexpr int kBarriers = 2 * (int)kK + 3 * (int)kV + 18;
-  static constexpr int kSmem = 1024 + kBarOff + kBarriers * 8 + 16 + kFlags * 4 + 8;
+  static constexpr int kWalkOff = kBarOff + (kBarriers * 8 + 16 + kFlags * 4 + 8 + 15) / 16 * 16;
+  static constexpr int kSmem = 1024 + kWalkOff + 32 * (kThreads / 32 + 2);
   static_assert(kSmem <= 227 * 1024, "shared memory");
   // TMEM columns: two streams' S (and P over it), two streams' O.
   static constexpr uint32_t kS = 0, kO = 256, kTmemCols = 512;
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
   tc_after_sync();
   pdl_trigger();  // only now: a successor that takes TMEM must not start before this CTA has its own
   const uint32_t tmem = *tslot;
-  Walk w(a);
+  Walk w(a, sm + S::kWalkOff + 32 * warp);
   Item it;
 
   if (warp >= kMmaWarp) {
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       const uint64_t qd = smem_desc(smem_addr(sm + t * S::kTileBytes), 16, 1024, kSw128);
       const uint64_t kd = smem_desc(smem_addr(sm + S::kKOff), 16, 1024, kSw128);
       const uint64_t vd = smem_desc(smem_addr(sm + S::kVOff), S::kHalfBytes, 1024, kSw128);
-      Walk ws(a);          // of the scores, a step ahead
+      Walk ws(a, sm + S::kWalkOff + kThreads + 32 * t);  // of the scores, a step ahead
       Item is{};
       int sb = 0;          // their next block in the item
       uint32_t items = 0, steps = 0, turns = t == 0 ? 1 : 0;
@@ -192,10 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         for (int b = b0; b < it.blocks; b += d, ++steps) {
           const uint32_t pos = w.pos + b, slot = pos % S::kV;
           const uint64_t vd_now = vd + slot * (S::kTileBytes >> 4);
-          // The next step's operands are asked for ahead of this one's weights, but where they are another unit's: its Q
-          // is loaded only now, and this unit's last product must not wait for it.
-          const bool ahead = sb < is.blocks;
-          if (!(ok = (!ahead || operands()) && await(&fixed[slot], pos / S::kV & 1, a.err, kErrAttn) &&
+          if (!(ok = operands() && await(&fixed[slot], pos / S::kV & 1, a.err, kErrAttn) &&
                      await(&pfull[2 * t], steps & 1, a.err, kErrAttn)))
             break;
           // Streams of two tiles take turns: left alone they fall into step, and the tensor core idles while both take
@@ -207,14 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           tc_after_sync();
           mma_pv4(to, ts + 32, vd_now + (64 * 128 >> 4), 128, id_o, 1);
           if (b + d >= it.blocks) mma_commit_elect(&ofull[t]);
-          if (ahead) scores();
+          if (more) scores();
           if (it.pair && lane == 0) mbar_arrive(&go[t ^ 1]);
           mma_commit_elect(&vfree[slot]);
           if (!it.pair) mma_commit_elect(&vfree[slot]);
-          if (!ahead) {
-            if (!(ok = operands())) break;
-            if (more) scores();
-          }
           if (more) scores_done();
         }
         w.done(it);
@@ -397,28 +391,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         const float base = m == -INFINITY ? 0.f : m;
         const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        uint32_t p[32];
-        auto weight = [&](int x, int y) {  // weights 2 x and 2 x + 1 of the row, to p[y]
-          float2 e = fma2(make_float2(s[2 * x], s[2 * x + 1]), c2, b2);
-          e.x = ex2(e.x);
-          e.y = ex2(e.y);
-          sum[x & 1] = add2(sum[x & 1], e);
-          p[y] = pack_bf16(e.x, e.y);
+        auto weights = [&](int x0) {  // 32 of the row's weights, to where the MMA takes them from
+          uint32_t p[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float2 e = fma2(make_float2(s[x0 + 2 * x], s[x0 + 2 * x + 1]), c2, b2);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum[x & 1] = add2(sum[x & 1], e);
+            p[x] = pack_bf16(e.x, e.y);
+          }
+          tmem_st16u(ts + x0 / 2, p);
         };
-#pragma unroll
-        for (int x = 0; x < 32; ++x) weight(x, x);
-        tmem_st32(ts, p);
-        tmem_wait_st();
-        tc_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[2 * t]);
-#pragma unroll
-        for (int x = 0; x < 32; ++x) weight(32 + x, x);
-        tmem_st32(ts + 32, p);
-        tmem_wait_st();
-        tc_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[2 * t + 1]);
+        auto ready = [&](int h) {
+          tmem_wait_st();
+          tc_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pfull[2 * t + h]);
+        };
+        weights(0);
+        weights(32);
+        ready(0);
+        weights(64);
+        weights(96);
+        ready(1);
         sum[0] = add2(sum[0], sum[1]);
         l += sum[0].x + sum[0].y;
       }

@@ -50,6 +50,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
         "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -115,28 +122,34 @@ struct Item {
   bool pair;
 };
 
+// One warp's walk; every lane calls. The next item's record comes by cp.async into 32 bytes of shared memory of the
+// warp's own (in registers, it was waited for and spilled ahead of the current item).
 struct Walk {
   const AttnArgs &a;
+  int4 *record;
   uint32_t n, at, k = 0;
   uint32_t pos = 0;      // blocks before the current item: block b of one tile belongs to stream (pos + b) & 1
   uint32_t index = 0;    // items before it
-  int4 r0, r1;           // the next item's record
-  __device__ __forceinline__ explicit Walk(const AttnArgs &args)
-      : a(args), n(~0u) {
+  __device__ __forceinline__ Walk(const AttnArgs &args, void *slot) : a(args), record(static_cast<int4 *>(slot)), n(~0u) {
     fetch();  // the first record with the number of units, not behind it: the plan has room for a unit of each CTA
     n = (uint32_t)args.plan[AttnPlan::kUnits] * (uint32_t)args.s.Hkv;
   }
+  static __device__ __forceinline__ uint32_t at_of(uint32_t k) {
+    return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  }
   __device__ __forceinline__ void fetch() {
-    at = k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    if (at < n) {
-      const int4 *p = reinterpret_cast<const int4 *>(a.plan + a.p.units() + (int64_t)AttnPlan::kUnit * (at / (uint32_t)a.s.Hkv));
-      r0 = p[0];
-      r1 = p[1];
-    }
+    at = at_of(k);
+    const uint32_t lane = threadIdx.x & 31;
+    if (at < n && lane < 2)
+      cp_async16(record + lane, a.plan + a.p.units() + (int64_t)AttnPlan::kUnit * (at / (uint32_t)a.s.Hkv) + 4 * lane);
   }
   // False at the end. Call done() after each item.
   __device__ __forceinline__ bool item(Item &it) {
     if (at >= n) return false;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    const int4 r0 = record[0], r1 = record[1];
+    __syncwarp();
     it.u = AttnUnit{r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
     it.head = (int)(at % (uint32_t)a.s.Hkv);
     it.blocks = it.u.kb1 - it.u.kb0;
@@ -145,8 +158,9 @@ struct Walk {
     fetch();
     return true;
   }
-  __device__ __forceinline__ void done(const Item &it) {
-    pos += it.blocks;
+  __device__ __forceinline__ void done(const Item &it) { done(it.blocks); }
+  __device__ __forceinline__ void done(int blocks) {
+    pos += blocks;
     ++index;
   }
   // Stream t's blocks of the item: from first(t) on, every step(it)-th one.
@@ -194,6 +208,25 @@ __device__ __forceinline__ bool fix_values(unsigned char *block, int half_bytes,
 #pragma unroll 1
   for (int i = r1 * kChunks + me; i < ((r1 + 15) & ~15) * kChunks; i += of) *chunk(i) = make_uint4(0, 0, 0, 0);
   return bad;
+}
+
+// What fix_values took out of column d of the unit's values, for a row that sees keys up to `end`: next to it, what is
+// finite does not count. Zero where nothing was.
+__device__ __forceinline__ float taken_out(const AttnArgs &a, const AttnUnit &u, int head, int d, int seen, int end) {
+  float sum = 0.f;
+  for (int j = max(seen, u.kb0 * kKeyBlock); j < min(end, u.kb1 * kKeyBlock); ++j) {
+    int64_t at;
+    if (a.kv.page_size > 0) {
+      const int page = a.kv.table[(int64_t)u.seq * a.kv.ld_table + (j >> a.kv.log2_page)];
+      if ((unsigned)page >= (unsigned)a.kv.num_pages) continue;
+      at = page * a.kv.v_page + (j & (a.kv.page_size - 1)) * a.kv.v_row;
+    } else {
+      at = ((int64_t)u.row0 - u.pos0 + j) * a.kv.v_row;
+    }
+    const float f = __bfloat162float(static_cast<const __nv_bfloat16 *>(a.kv.v)[at + head * a.kv.v_head + d]);
+    if (!isfinite(f)) sum += f;
+  }
+  return sum;
 }
 
 // ------------------------------------------------------------------ host side
