@@ -603,8 +603,9 @@ size_t lora_seqs_plan_bytes(const lora_seqs *seqs);
  * rows of keys are split, and the parts joined when all are done. A sequence
  * whose rows are not within [0, num_tokens], or whose keys are negative, more
  * than max_pages * page_size (where there is a cache) or more than
- * LORA_MAX_KV_LEN, is treated as empty and counted (lora_query_seqs). One call
- * a step serves all layers of the geometry.
+ * LORA_MAX_KV_LEN, is treated as empty and counted (lora_query_seqs); a row
+ * that two sequences hold (q_start falls) gets the result of one of them. One
+ * call a step serves all layers of the geometry.
  * Errors: null pointers, a plan that is too small, a head_dim that is no
  * multiple of 8, kv heads that do not divide the heads, a scale that is not
  * positive and finite, an invalid page_size -> LORA_EINVAL; counts outside

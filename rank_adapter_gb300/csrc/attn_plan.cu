@@ -8,7 +8,7 @@
 // size is the even share of a CTA, total cost x heads / CTAs, where there are many
 // units; where there are few, 32 sizes around it are tried, a warp each, and the one
 // is taken whose rounds of CTAs end first (three sequences of 110 thousand keys: 168
-// pieces of a share on 152 CTAs 299 us, 144 larger ones TODO us). One CTA does it
+// pieces of a share on 152 CTAs 299 us, 144 larger ones 213). One CTA does it
 // all; it is latency, which a step pays once for all layers.
 //
 // Cache write: a warp a row, all of its 16-byte loads in flight before the first
@@ -33,11 +33,12 @@ AttnShape attn_shape(const lora_seqs &q) {
   s.unit_tokens = s.tc ? 2 * s.tile_tokens : s.tile_tokens;
   s.slot_rows = s.tc ? 256 : std::max(32, s.G);
   // Units of few rows where a sequence has up to kFewRows rows on average, of the least size that takes a token of every
-  // sequence, or twice the average where there are more. (256 requests of a token by 4 heads a group: 306 us, 429 as tiles
+  // sequence, or 1.4 times the average where there are more (48 drafts of 1 to 5 tokens by 7 heads: 24.4 us in units of 32
+  // rows, 29.3 in units of 64). (256 requests of a token by 4 heads a group: 306 us, 429 as tiles
   // of 128 rows. A prompt of 500 tokens by 4: 20.9 us in units of 64 rows, 16.0 as tiles.)
   const int64_t rows = (int64_t)q.num_tokens * s.G;
   if (s.tc && s.G <= 64 && rows <= (int64_t)kFewRows * q.num_seqs) {
-    const int64_t want = std::max<int64_t>(s.G, q.num_tokens > q.num_seqs ? 2 * rows / q.num_seqs : 0);
+    const int64_t want = std::max<int64_t>(s.G, q.num_tokens > q.num_seqs ? 7 * rows / 5 / q.num_seqs : 0);
     s.few = want <= 16 ? 16 : want <= 32 ? 32 : 64;
     s.unit_tokens = s.few / s.G;
     s.slot_rows = s.few;
@@ -66,8 +67,8 @@ size_t attn_plan_bytes(const lora_seqs &q) {
   const AttnShape s = attn_shape(q);
   AttnPlan p = attn_plan(s, q.num_seqs, q.num_tokens);
   if (s.tc) {
-    // Units of few rows: sequences make one each, and one for each unit_tokens of the batch's tokens, which are at most
-    // 1.07 a sequence (twice the average of tokens in half of a unit's room, or a token a sequence).
+    // Units of few rows: sequences make one each, and one for each unit_tokens of the batch's tokens, which are less than
+    // two a sequence (a unit has room for 1.4 times the average of rows and holds more than half of it, or for a token).
     const int long_tokens = 2 * (128 / s.G);
     p.max_units = (int)std::max<int64_t>(q.num_tokens / long_tokens + q.num_seqs,
                                          std::min<int64_t>((int64_t)q.num_tokens + q.num_seqs, 3ll * q.num_seqs)) + s.max_slots + 1;
@@ -94,51 +95,50 @@ struct PlanArgs {
   int32_t *plan;
 };
 
+// What the CTA's warps tell one another in a scan. Calls take its two halves in turn, so that each needs one barrier: a
+// warp writes a half again only behind the next call's barrier, which the last readers of it have passed.
+struct ScanRoom {
+  unsigned long long part[2][kThreads / 32];
+  int top[2][kThreads / 32];
+};
+
 // Exclusive sum over the CTA's threads; *total gets the sum of all.
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, unsigned long long *part,
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, ScanRoom &room, uint32_t &turn,
                                                          unsigned long long *total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long incl = v;
+  unsigned long long incl = v, *part = room.part[turn++ & 1];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const unsigned long long u = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += u;
   }
-  __syncthreads();  // the previous call's reads of part
   if (lane == 31) part[warp] = incl;
   __syncthreads();
-  if (warp == 0) {
-    unsigned long long w = part[lane];
+  unsigned long long w = part[lane];  // every warp: the sums up to each warp's
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long u = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += u;
-    }
-    part[lane] = w;
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
   }
-  __syncthreads();
-  *total = part[31];
-  return incl - v + (warp > 0 ? part[warp - 1] : 0ull);
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const unsigned long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  return incl - v + (warp > 0 ? before : 0ull);
 }
 
 // The largest value of this and the CTA's earlier threads; *most gets that of all.
-__device__ __forceinline__ int block_max(int v, int *part, int *most) {
+__device__ __forceinline__ int block_max(int v, ScanRoom &room, uint32_t &turn, int *most) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int *top = room.top[turn++ & 1];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v = max(v, u);
   }
-  __syncthreads();  // the previous call's reads of part
-  if (lane == 31) part[warp] = v;
+  if (lane == 31) top[warp] = v;
   __syncthreads();
-  int before = INT32_MIN, all = INT32_MIN;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before = max(before, part[w]);
-    all = max(all, part[w]);
-  }
-  *most = all;
-  return max(v, before);
+  const int other = top[lane];
+  *most = __reduce_max_sync(0xffffffffu, other);
+  return max(v, __reduce_max_sync(0xffffffffu, lane < warp ? other : INT32_MIN));
 }
 
 struct Cut {  // a unit before it is split
@@ -166,12 +166,14 @@ __device__ __forceinline__ Cut cut_of(const PlanArgs &a, const int32_t *cum, con
 }
 
 __global__ void __launch_bounds__(kThreads) prepare_seqs_kernel(const PlanArgs a) {
-  __shared__ unsigned long long part[32], total_cost;
-  __shared__ int bins[kBins], maxima[kThreads / 32], bad, most, groups, sizes[kThreads / 32], costs[kThreads];
+  __shared__ ScanRoom room;
+  __shared__ unsigned long long total_cost;
+  __shared__ int bins[kBins], bad, most, groups, sizes[kThreads / 32], costs[kThreads];
   __shared__ float ends[kThreads / 32];
   __shared__ int4 near_seqs[kNear];
   __shared__ int32_t near_cum[kNear];
   const int tid = threadIdx.x;
+  uint32_t turn = 0;
   int32_t *const out_cum = a.plan + a.p.cum();
   int4 *const out_seqs = reinterpret_cast<int4 *>(a.plan + a.p.seqs());
   const bool near = a.S <= kNear;
@@ -202,9 +204,9 @@ __global__ void __launch_bounds__(kThreads) prepare_seqs_kernel(const PlanArgs a
       row = good ? r0 : 0;
     }
     int most_row;
-    row = max(first, block_max(row, maxima, &most_row));  // a sequence treated as empty starts with its predecessor
+    row = max(first, block_max(row, room, turn, &most_row));  // a sequence treated as empty starts with its predecessor
     first = max(first, most_row);
-    const unsigned long long before = base + block_scan(u, part, &total);
+    const unsigned long long before = base + block_scan(u, room, turn, &total);
     if (b < a.S) {
       cum[b] = (int)min(before, (unsigned long long)INT32_MAX);
       a.plan[a.p.start() + b] = row;
@@ -213,9 +215,9 @@ __global__ void __launch_bounds__(kThreads) prepare_seqs_kernel(const PlanArgs a
   }
   // Sequences that overlap (q_start out of order) can make more units than there is room
   // for: the last of them are dropped.
-  const int room = a.p.max_units - a.s.max_slots;
-  if (tid == 0 && base > (unsigned long long)room) atomicAdd(&bad, 1);
-  const int n = (int)min(base, (unsigned long long)room);
+  const int most_units = a.p.max_units - a.s.max_slots;
+  if (tid == 0 && base > (unsigned long long)most_units) atomicAdd(&bad, 1);
+  const int n = (int)min(base, (unsigned long long)most_units);
   __syncthreads();
   unsigned long long mine = 0;
   int top = 0;
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(kThreads) prepare_seqs_kernel(const PlanArgs a
         pieces = c.cost > chunk ? (int)min((int64_t)c.blocks, (c.cost + piece - 1) / piece) : 1;
       }
       const bool wants = pieces > 1;
-      const unsigned long long at = base + block_scan(wants ? (unsigned long long)pieces : 0ull, part, &total);
+      const unsigned long long at = base + block_scan(wants ? (unsigned long long)pieces : 0ull, room, turn, &total);
       base += total;
       const bool split = wants && at + pieces <= (unsigned long long)a.s.max_slots;
       if (i >= n) continue;
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) prepare_seqs_kernel(const PlanArgs a
     __syncthreads();
     if (pass == 0) {
       const unsigned long long v = tid < kBins ? (unsigned long long)bins[tid] : 0ull;
-      const unsigned long long at = block_scan(v, part, &total);
+      const unsigned long long at = block_scan(v, room, turn, &total);
       if (tid < kBins) bins[tid] = (int)at;
       if (tid == 0) a.plan[AttnPlan::kUnits] = (int)total;
       __syncthreads();
