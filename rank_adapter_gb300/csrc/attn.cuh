@@ -95,6 +95,7 @@ __host__ __device__ inline int64_t slot_floats(const AttnShape &s) { return (int
 
 AttnShape attn_shape(const lora_seqs &q);
 AttnPlan attn_plan(const AttnShape &s, int num_seqs, int num_tokens);
+int64_t attn_slot_rows(const lora_seqs &q);  // rows of partial results of one key-value head, likewise
 size_t attn_plan_bytes(const lora_seqs &q);  // enough for up to so many sequences and rows, however units are cut
 bool attn_may_split(const AttnShape &s, int64_t max_kv);
 

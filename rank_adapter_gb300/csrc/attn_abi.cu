@@ -112,8 +112,7 @@ size_t lora_seqs_plan_bytes(const lora_seqs *seqs) {
 size_t lora_attn_workspace_bytes(const lora_seqs *seqs) {
   if (check_shape(seqs) != LORA_OK) return 0;
   const ra::AttnShape s = ra::attn_shape(*seqs);
-  const int64_t rows = s.tc ? 256 : s.slot_rows;  // whichever way units are cut
-  return (size_t)(s.max_slots * s.Hkv * rows * (s.D + 2)) * sizeof(float);
+  return (size_t)(ra::attn_slot_rows(*seqs) * s.Hkv * (s.D + 2)) * sizeof(float);
 }
 
 int lora_prepare_seqs(const lora_seqs *seqs, lora_stream_t stream) {

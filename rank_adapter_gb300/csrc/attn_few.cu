@@ -4,7 +4,7 @@
 //
 // The keys take the MMA's long side and a unit's N = 16, 32 or 64 rows (token, query head)
 // its short one, so that little is computed for rows that are not there, and shared memory
-// goes to blocks in flight (3 of K and 3 or 2 of V, 160 to 192 KB):
+// goes to blocks in flight, 160 to 192 KB of an SM:
 //   S^T = K Q^T     128 keys by N, in TMEM, a thread a key
 //   P^T = 2^(c S^T - m)    bf16, to shared memory, a thread its key's N weights
 //   O^T += V^T P^T  128 elements of the head by N, in TMEM, a thread an element (a head of
@@ -15,14 +15,18 @@
 // barrier a block) that some weight exceeds 2^24. Sums stay with the keys' threads until a
 // unit's end. (With the maximum over the keys at each unit's first block, and bases held
 // within 2^8, three requests of 110 thousand keys took as long, one of 999 keys 0.8 us more.)
-// The scores of the next block are issued before the product of this one.
+// Scores and products are issued by a warp each. Units of 16 rows leave room for two CTAs
+// of an SM with three (heads of 64: six) blocks in flight each, so that one's waits and
+// ends of units are the other's time (five requests of 21 thousand keys, 20 heads of 64:
+// 123 us with one warp for all MMAs, 119 with two, 89 with two CTAs; 232 requests of a few
+// keys by 8 heads of 128 34, 34 and 20 us).
 #include "attn_tc.cuh"
 
 namespace ra {
 namespace {
 
 constexpr int kKeys = 128;
-constexpr int kMmaWarp = 4, kKWarp = 5, kVWarp = 6, kFixWarp = 7, kThreads = 256;
+constexpr int kScoreWarp = 4, kKWarp = 5, kVWarp = 6, kProductWarp = 7, kThreads = 256;
 constexpr float kLazy = 24.f;     // log2 of the factor that a weight may exceed 1 by
 constexpr float kLowest = -3e38f; // base of a row without a key so far
 constexpr int kFlags = 8;         // units that the loads can be ahead of an epilogue, and more
@@ -31,7 +35,10 @@ template <int N_, int D_>
 struct FewShape {
   static constexpr int N = N_, D = D_, kHalves = D / 64;
   static constexpr int kHalfBytes = kKeys * 128, kTileBytes = kHalves * kHalfBytes;  // a K or V block, 64 elements at a time
-  static constexpr uint32_t kK = D == 64 ? 6 : 3, kV = D == 64 ? 5 : N == 64 ? 2 : 3, kQ = 2, kP = N == 64 ? 1 : 2;
+  // CTAs of an SM: two, with half of the blocks in flight each, where that leaves room for enough of them.
+  static constexpr int kCtas = N == 16 ? 2 : 1;
+  static constexpr uint32_t kK = N == 16 ? (D == 64 ? 3 : 2) : (D == 64 ? 6 : 3), kV = N == 16 ? (D == 64 ? 3 : 1) : D == 64 ? 5 : N == 64 ? 2 : 3;
+  static constexpr uint32_t kQ = N == 16 && D == 128 ? 1 : 2, kP = N == 64 || (N == 16 && D == 128) ? 1 : 2;
   static constexpr int kQHalf = N * 128, kQBytes = kHalves * kQHalf, kPBytes = kKeys * N * 2;
   static constexpr uint32_t kPLayout = N == 16 ? kSw32 : N == 32 ? kSw64 : kSw128;
   static constexpr int kKOff = 0, kVOff = kKOff + (int)kK * kTileBytes, kQOff = kVOff + (int)kV * kTileBytes;
@@ -39,11 +46,11 @@ struct FewShape {
   static constexpr int kRowOff = kPOff + (int)kP * kPBytes;   // of each row: base, factor, keys, and where it goes
   static constexpr int kWarpOff = kRowOff + N * 20 + 16 - N * 20 % 16;  // a value of each row from each warp
   static constexpr int kBarOff = kWarpOff + 4 * N * 4;
-  static constexpr int kBarriers = 2 * (int)kK + 3 * (int)kV + 2 * (int)kQ + 2 + 2 * (int)kP + 1;
+  static constexpr int kBarriers = 2 * (int)kK + 2 * (int)kV + 2 * (int)kQ + 4 + 2 * (int)kP + 2;
   static constexpr int kWalkOff = kBarOff + (kBarriers * 8 + 16 + kFlags * 4 + 15) / 16 * 16;
-  static constexpr int kEnd = kWalkOff + 32 * (kThreads / 32 + 1);
+  static constexpr int kEnd = kWalkOff + 32 * (kThreads / 32);
   static constexpr int kSmem = 1024 + (kEnd > kQOff + kHalfBytes ? kEnd : kQOff + kHalfBytes);  // what the MMA reads behind V, too
-  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory");
   static constexpr uint32_t kO = 2 * N, kTmemCols = N == 16 ? 64 : N == 32 ? 128 : 256;  // TMEM: two S, then O
 };
 
@@ -87,7 +94,7 @@ __device__ __forceinline__ void store_across(float *to, const float (&v)[N], int
 }
 
 template <int N, int D, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_constant__ FewMaps maps, const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, (FewShape<N, D>::kCtas)) attn_few_kernel(const __grid_constant__ FewMaps maps, const AttnArgs a) {
   using S = FewShape<N, D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char *sm = align1024(smem_raw);
@@ -95,14 +102,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
   uint64_t *kfree = kfull + S::kK;       // its scores are done
   uint64_t *vfull = kfree + S::kK;       // a V block is in
   uint64_t *vfree = vfull + S::kV;       // its product is done
-  uint64_t *fixed = vfree + S::kV;       // it has been looked at
-  uint64_t *qfull = fixed + S::kV;       // a unit's Q is in
+  uint64_t *qfull = vfree + S::kV;       // a unit's Q is in
   uint64_t *qfree = qfull + S::kQ;       // its last scores are done
   uint64_t *sfull = qfree + S::kQ;       // a block's S^T is in TMEM
-  uint64_t *pfull = sfull + 2;           // its P^T is in shared memory
+  uint64_t *sread = sfull + 2;           // it has been read
+  uint64_t *pfull = sread + 2;           // a block's P^T is in shared memory
   uint64_t *pfree = pfull + S::kP;       // its product is done
   uint64_t *fin = pfree + S::kP;
-  uint32_t *tslot = reinterpret_cast<uint32_t *>(fin + 1);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(fin + 2);
   volatile int32_t *flags = reinterpret_cast<int32_t *>(tslot + 1);  // [item % kFlags]: the last item with values taken out
   int64_t *to_row = reinterpret_cast<int64_t *>(sm + S::kRowOff);    // byte offsets of the rows in the output, -1 for none
   float *base = reinterpret_cast<float *>(to_row + N), *factor = base + N;
@@ -117,7 +124,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
     for (uint32_t i = 0; i < S::kV; ++i) {
       mbar_init(&vfull[i], 1);
       mbar_init(&vfree[i], 1);
-      mbar_init(&fixed[i], 1);
     }
     for (uint32_t i = 0; i < S::kQ; ++i) {
       mbar_init(&qfull[i], 1);
@@ -127,13 +133,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
       mbar_init(&pfull[i], 4);
       mbar_init(&pfree[i], 1);
     }
-    mbar_init(&sfull[0], 1);
-    mbar_init(&sfull[1], 1);
-    mbar_init(fin, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&sread[i], 4);
+      mbar_init(&fin[i], 1);
+    }
     for (int i = 0; i < kFlags; ++i) flags[i] = -1;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) tmem_alloc(tslot, S::kTmemCols);
+  if (warp == kScoreWarp) tmem_alloc(tslot, S::kTmemCols);
   if (warp == kKWarp && lane < 2) prefetch_map(lane == 0 ? &maps.k : &maps.q);
   if (warp == kVWarp && lane == 0) prefetch_map(&maps.v);
   // Rows of Q that no unit has: zeros, which raise no base.
@@ -149,63 +157,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
   Walk w(a, sm + S::kWalkOff + 32 * warp);
   Item it;
 
-  if (warp == kMmaWarp) {
-    // ---- MMA issue
-    constexpr uint32_t id_s = idesc_kk(kKeys, N), id_o = idesc_bf16(128, N) | (1u << 15);  // both operands as they lie
+  if (warp == kScoreWarp) {
+    // ---- scores
+    constexpr uint32_t id_s = idesc_kk(kKeys, N);
     const uint64_t kd = smem_desc(smem_addr(sm + S::kKOff), 16, 1024, kSw128), qd = smem_desc(smem_addr(sm + S::kQOff), 16, 1024, kSw128);
-    // (With one half, the MMA's other 64 rows come from the next block or from Q, and go nowhere.)
-    const uint64_t vd = smem_desc(smem_addr(sm + S::kVOff), S::kHalfBytes, 1024, kSw128);
-    const uint64_t pd = smem_desc(smem_addr(sm + S::kPOff), 16, 16 * N, S::kPLayout);
-    Walk ws(a, sm + S::kWalkOff + kThreads);  // of the scores, a block ahead
-    Item is{};
-    int sb = 0;
-    bool more = ws.item(is);
-    uint32_t gs = 0, g = 0, items = 0;  // blocks scored, blocks multiplied, units with scores begun
-    auto scores = [&]() -> bool {
-      while (more && sb >= is.blocks) {
-        more = ws.item(is);
-        sb = 0;
-      }
-      if (!more) return true;
-      if (sb == 0) {
-        if (!await(&qfull[items % S::kQ], items / S::kQ & 1, a.err, kErrAttn)) return false;
-        ++items;
-      }
-      const uint32_t slot = gs % S::kK, qs = (items - 1) % S::kQ;
-      if (!await(&kfull[slot], gs / S::kK & 1, a.err, kErrAttn)) return false;
-#pragma unroll
-      for (int h = 0; h < S::kHalves; ++h)
-        mma_run<4>(tmem + (gs & 1) * N, kd + slot * (S::kTileBytes >> 4) + h * (S::kHalfBytes >> 4),
-                   qd + qs * (S::kQBytes >> 4) + h * (S::kQHalf >> 4), 2, 2, id_s, h > 0);
-      mma_commit_elect(&sfull[gs & 1]);
-      mma_commit_elect(&kfree[slot]);
-      ++gs;
-      if (++sb == is.blocks) mma_commit_elect(&qfree[qs]);
-      return true;
-    };
-    bool ok = scores();
+    uint32_t g = 0, items = 0;  // blocks, and units with any, so far
+    bool ok = true;
     while (ok && w.item(it)) {
+      if (it.blocks == 0) continue;
+      const uint32_t qs = items % S::kQ;
+      if (!await(&qfull[qs], items / S::kQ & 1, a.err, kErrAttn)) break;
+      ++items;
       for (int b = 0; b < it.blocks; ++b, ++g) {
-        // The next scores' place in TMEM is free: the weights of the block before this one, made of it, have been seen.
-        const uint32_t slot = g % S::kV, ps = g % S::kP;
-        ok = scores() && await(&fixed[slot], g / S::kV & 1, a.err, kErrAttn) && await(&pfull[ps], g / S::kP & 1, a.err, kErrAttn);
-        if (!ok) break;
+        const uint32_t slot = g % S::kK;
+        if (!(ok = await(&kfull[slot], g / S::kK & 1, a.err, kErrAttn) && await(&sread[g & 1], (g >> 1 & 1) ^ 1, a.err, kErrAttn))) break;
         tc_after_sync();
-        const uint64_t vs = vd + slot * (S::kTileBytes >> 4), pp = pd + ps * (S::kPBytes >> 4);
-        const int keys = it.u.kv_len - (it.u.kb0 + b) * kKeyBlock;
-        if (keys >= kKeys) {
-          mma_run<4>(tmem + S::kO, vs, pp, 128, 2 * N, id_o, b > 0);
-          mma_run<4>(tmem + S::kO, vs + 4 * 128, pp + 8 * N, 128, 2 * N, id_o, 1);
-        } else {
-#pragma unroll 1
-          for (int s = 0; s * 16 < keys; ++s) mma_run<1>(tmem + S::kO, vs + s * 128, pp + s * 2 * N, 0, 0, id_o, b > 0 || s > 0);
-        }
-        mma_commit_elect(&pfree[ps]);
-        mma_commit_elect(&vfree[slot]);
+#pragma unroll
+        for (int h = 0; h < S::kHalves; ++h)
+          mma_run<4>(tmem + (g & 1) * N, kd + slot * (S::kTileBytes >> 4) + h * (S::kHalfBytes >> 4),
+                     qd + qs * (S::kQBytes >> 4) + h * (S::kQHalf >> 4), 2, 2, id_s, h > 0);
+        mma_commit_elect(&sfull[g & 1]);
+        mma_commit_elect(&kfree[slot]);
       }
+      mma_commit_elect(&qfree[qs]);
     }
-    mma_commit_elect(fin);
-    await(fin, 0, a.err, kErrAttn);  // every MMA is done before TMEM is freed
+    mma_commit_elect(&fin[0]);
+    await(&fin[0], 0, a.err, kErrAttn);  // every MMA is done before TMEM is freed
   } else if (warp == kKWarp || warp == kVWarp) {
     // ---- loads: one warp Q and K blocks, one V blocks
     const bool keys = warp == kKWarp;
@@ -259,30 +236,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
         }
       }
     }
-  } else if (warp == kFixWarp) {
-    // ---- values that not every row sees (see attn_tc.cu): rows behind the keys are zeroed up to the last MMA's end
-    uint32_t slot = 0, phase = 0;
+  } else if (warp == kProductWarp) {
+    // ---- products, once the values that not every row sees have been looked at: rows behind the keys are zeroed up to the
+    // last MMA's end
+    constexpr uint32_t id_o = idesc_bf16(128, N) | (1u << 15);  // both operands as they lie
+    // (With one half, the MMA's other 64 rows come from the next block or from Q, and go nowhere.)
+    const uint64_t vd = smem_desc(smem_addr(sm + S::kVOff), S::kHalfBytes, 1024, kSw128);
+    const uint64_t pd = smem_desc(smem_addr(sm + S::kPOff), 16, 16 * N, S::kPLayout);
+    uint32_t g = 0;
     bool ok = true;
     while (ok && w.item(it)) {
       const int seen = common_keys(it.u, a.s.causal);
-      for (int b = 0; b < it.blocks; ++b) {
-        const int j0 = (it.u.kb0 + b) * kKeyBlock;
-        if (!await(&vfull[slot], phase, a.err, kErrAttn)) { ok = false; break; }
+      for (int b = 0; b < it.blocks; ++b, ++g) {
+        const uint32_t slot = g % S::kV, ps = g % S::kP;
+        const int j0 = (it.u.kb0 + b) * kKeyBlock, keys = it.u.kv_len - j0;
+        if (!(ok = await(&vfull[slot], g / S::kV & 1, a.err, kErrAttn))) break;
         if (j0 + kKeyBlock > seen) {
-          if (fix_values<D>(sm + S::kVOff + slot * S::kTileBytes, S::kHalfBytes, max(0, seen - j0), min(kKeyBlock, it.u.kv_len - j0),
-                            lane, 32))
+          if (fix_values<D>(sm + S::kVOff + slot * S::kTileBytes, S::kHalfBytes, max(0, seen - j0), min(kKeyBlock, keys), lane, 32))
             flags[w.index % kFlags] = (int)w.index;
           fence_async_smem();
+          __syncwarp();
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&fixed[slot]);
-        if (++slot == S::kV) {
-          slot = 0;
-          phase ^= 1;
+        if (!(ok = await(&pfull[ps], g / S::kP & 1, a.err, kErrAttn))) break;
+        tc_after_sync();
+        const uint64_t vs = vd + slot * (S::kTileBytes >> 4), pp = pd + ps * (S::kPBytes >> 4);
+        if (keys >= kKeys) {
+          mma_run<4>(tmem + S::kO, vs, pp, 128, 2 * N, id_o, b > 0);
+          mma_run<4>(tmem + S::kO, vs + 4 * 128, pp + 8 * N, 128, 2 * N, id_o, 1);
+        } else {
+#pragma unroll 1
+          for (int s = 0; s * 16 < keys; ++s) mma_run<1>(tmem + S::kO, vs + s * 128, pp + s * 2 * N, 0, 0, id_o, b > 0 || s > 0);
         }
+        mma_commit_elect(&pfree[ps]);
+        mma_commit_elect(&vfree[slot]);
       }
       w.done(it);
     }
+    mma_commit_elect(&fin[1]);
+    await(&fin[1], 0, a.err, kErrAttn);
   } else {
     // ---- weights: a thread a key; and the outputs: a thread an element of the head
     const int tid = threadIdx.x;
@@ -321,6 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
           for (int x = 0; x < N; x += 32) tmem_ld32_async(lanes + (g & 1) * N + x, s + x);
           tmem_wait_ld();
         }
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sread[g & 1]);
         if ((it.u.kb0 + b + 1) * kKeyBlock > seen) {
 #pragma unroll
           for (int n = 0; n < N; ++n) s[n] = j < sees[n] ? s[n] : -INFINITY;
@@ -441,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const __grid_cons
   }
   tc_before_sync();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     tc_after_sync();
     tmem_free(tmem, S::kTmemCols);
   }

@@ -43,14 +43,14 @@ AttnShape attn_shape(const lora_seqs &q) {
     s.unit_tokens = s.few / s.G;
     s.slot_rows = s.few;
   }
-  s.ctas = (s.tc ? 1 : 2) * std::max(1, sm_count());
+  s.ctas = (s.tc && s.few != 16 ? 1 : 2) * std::max(1, sm_count());
   s.min_cost = 2;
-  // In blocks of keys by tiles, as measured: units of few rows take 1.5 us a block while all CTAs read, 0.86 us alone;
-  // one of two tiles takes 0.85 us a tile, whatever the others do.
-  s.alone = s.few > 0 ? 0.57f : 1.f;
+  // In blocks of keys by tiles, as measured: two CTAs of 16 rows take 3 us a block while all read, one alone about 1.1;
+  // one of 32 or 64 rows 1.5 and 0.86; one of two tiles 0.85 a tile, whatever the others do.
+  s.alone = s.few == 16 ? 0.35f : s.few > 0 ? 0.57f : 1.f;
   s.piece_cost = s.few > 0 ? 1.f : 5.f;
-  s.join_cost = s.few > 0 ? 2.5f : 8.f;
-  s.max_slots = 2 * s.ctas / s.Hkv + 2;
+  s.join_cost = s.few == 16 ? 0.8f : s.few > 0 ? 2.5f : 8.f;
+  s.max_slots = (s.few > 0 ? 4 : 2) * s.ctas / s.Hkv + 2;
   s.scale_log2 = (float)((double)q.scale * 1.4426950408889634);
   return s;
 }
@@ -63,8 +63,19 @@ AttnPlan attn_plan(const AttnShape &s, int num_seqs, int num_tokens) {
   return p;
 }
 
-size_t attn_plan_bytes(const lora_seqs &q) {
+// Partial results of a key-value head, however units are cut, and the rows of them all.
+int most_slots(const AttnShape &s) { return 8 * std::max(1, sm_count()) / s.Hkv + 2; }
+
+int64_t attn_slot_rows(const lora_seqs &q) {
   const AttnShape s = attn_shape(q);
+  if (!s.tc) return (int64_t)s.max_slots * s.slot_rows;
+  const int sms = std::max(1, sm_count());
+  return std::max({256ll * (2 * sms / s.Hkv + 2), 64ll * (4 * sms / s.Hkv + 2), 16ll * (8 * sms / s.Hkv + 2)});
+}
+
+size_t attn_plan_bytes(const lora_seqs &q) {
+  AttnShape s = attn_shape(q);
+  if (s.tc) s.max_slots = most_slots(s);
   AttnPlan p = attn_plan(s, q.num_seqs, q.num_tokens);
   if (s.tc) {
     // Units of few rows: sequences make one each, and one for each unit_tokens of the batch's tokens, which are less than
@@ -258,9 +269,9 @@ __global__ void __launch_bounds__(kThreads) prepare_seqs_kernel(const PlanArgs a
     if (lane == 0) {
       const int items = pieces * a.s.Hkv, rounds = (items + a.s.ctas - 1) / a.s.ctas, last = items - (rounds - 1) * a.s.ctas;
       const float average = (float)total_cost / (float)max(1, pieces);
-      const float even = ((float)(rounds - 1) + (2 * last > a.s.ctas ? 1.f : a.s.alone)) * average;
+      const float even = ((float)(rounds - 1) + a.s.alone + (1.f - a.s.alone) * (float)last / (float)a.s.ctas) * average;
       const float end = fmaxf((float)largest * a.s.alone, fminf(even, (float)share + (float)smallest));
-      ends[warp] = pieces - n > a.s.max_slots / 2 ? INFINITY : end + a.s.piece_cost * (float)rounds + (pieces > n ? a.s.join_cost : 0.f);
+      ends[warp] = pieces - n > a.s.max_slots / 2 ? INFINITY : end + a.s.piece_cost * (float)rounds + (pieces > n ? a.s.join_cost + 0.1f * (float)pieces / (float)n : 0.f);
       sizes[warp] = size;
     }
     __syncthreads();
