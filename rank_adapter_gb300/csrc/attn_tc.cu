@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (!more) return true;
         // A barrier's phases are told apart by their parity only. Where the slot's last block was the other stream's alone,
         // that one has to have been in before this stream may wait for the next.
-        if ((own >> slot & 1) == 0 && !__all_sync(0xffffffffu, past(&reached[t ^ 1], pos - S::kK, a.err, kErrAttn)))
+        if ((own >> slot & 1) == 0 && pos >= S::kK &&
+            !__all_sync(0xffffffffu, past(&reached[t ^ 1], pos - S::kK, a.err, kErrAttn)))
           return false;
         own |= 1u << slot;
         if (sb < ws.step(is) && !await(&qfull[t], items++ & 1, a.err, kErrAttn)) return false;
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       unsigned char *ring = sm + (keys ? S::kKOff : S::kVOff);
       const int half = lane % S::kHalves, part = lane / S::kHalves;
       uint32_t slot = 0, phase = 0, used0 = 0, used1 = 0;
-      bool ok = true;
+      bool ok = true, alone = false;  // alone: the unit before had one tile
       while (ok && w.item(it)) {
         for (int b = 0; b < it.blocks; ++b) {
           const int j0 = (it.u.kb0 + b) * kKeyBlock;
@@ -256,9 +257,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             slot = 0;
             phase ^= 1;
           }
-          if (!keys || b != min(1, it.blocks - 1)) continue;
+          if (!keys || b != (alone ? 0 : min(1, it.blocks - 1))) continue;
           // Q tiles, behind the first two K blocks, which need not wait for the previous unit's last scores: a
-          // stream's own where there are two, the same for both where there is one.
+          // stream's own where there are two, the same for both where there is one. Behind a unit of one tile only behind
+          // the first: the second may have to wait for a stream that waits for its turn, which the other gives it
+          // once its next unit's Q is in.
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             uint32_t &used = t == 0 ? used0 : used1;
@@ -273,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
           }
           if (!ok) break;
         }
+        alone = !it.pair;
         w.done(it);
       }
     } else {
@@ -438,7 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
       mine_used += mine;
       float w0 = 1.f, w1 = 0.f;  // weights of this stream's and the other's O
       if (merge) {
-        if (!await(&ofull[t ^ 1], other_used & 1, a.err, kErrAttn) || !await(mfull, merges & 1, a.err, kErrAttn)) { ok = false; break; }
+        // First the statistics: behind them the other stream has seen its last product of every unit before, so that the parity
+        // of its products' barrier stands for this unit's.
+        if (!await(mfull, merges & 1, a.err, kErrAttn) || !await(&ofull[t ^ 1], other_used & 1, a.err, kErrAttn)) { ok = false; break; }
         ++merges;
         const float2 o = stats[r];
         const float mm = fmaxf(m, o.x), base = mm == -INFINITY ? 0.f : mm;

@@ -129,7 +129,7 @@ struct Walk {
   int4 *record;
   uint32_t n, at, k = 0;
   uint32_t pos = 0;      // blocks before the current item: block b of one tile belongs to stream (pos + b) & 1
-  uint32_t index = 0;    // items before it
+  uint32_t index = 0;    // items with any before it
   __device__ __forceinline__ Walk(const AttnArgs &args, void *slot) : a(args), record(static_cast<int4 *>(slot)), n(~0u) {
     fetch();  // the first record with the number of units, not behind it: the plan has room for a unit of each CTA
     n = (uint32_t)args.plan[AttnPlan::kUnits] * (uint32_t)args.s.Hkv;
@@ -161,7 +161,7 @@ struct Walk {
   __device__ __forceinline__ void done(const Item &it) { done(it.blocks); }
   __device__ __forceinline__ void done(int blocks) {
     pos += blocks;
-    ++index;
+    index += blocks > 0;
   }
   // Stream t's blocks of the item: from first(t) on, every step(it)-th one.
   __device__ __forceinline__ int first(const Item &it, int t) const { return it.pair ? 0 : (int)((pos ^ (uint32_t)t) & 1u); }
