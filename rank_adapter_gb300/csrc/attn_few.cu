@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, (FewShape<N, D>::kCtas)) attn_few_ke
                       : it.u.slot >= 0
                           ? (((int64_t)it.u.slot * a.s.Hkv + it.head) * slot_floats(a.s) + (int64_t)tid * D) * 4
                           : (((int64_t)it.u.row0 + tok) * a.ldo + (int64_t)head * D) * 2;
-        base[tid] = kLowest;
+        base[tid] = live ? kLowest : INFINITY;  // rows of Q behind the unit's, another sequence's: weights 0, and no rise for them
       }
       keys_sync();
       float l[N];
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, (FewShape<N, D>::kCtas)) attn_few_ke
         if (b == 0) {
           if (tid == 0) {
 #pragma unroll
-            for (int n = 0; n < N; ++n) base[n] = s[n] == -INFINITY ? kLowest : s[n] * c;
+            for (int n = 0; n < N; ++n) base[n] = fmaxf(s[n] * c, base[n]);
           }
           keys_sync();
         }

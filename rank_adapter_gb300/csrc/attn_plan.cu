@@ -136,7 +136,7 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, S
   return incl - v + (warp > 0 ? before : 0ull);
 }
 
-// The largest value of this and the CTA's earlier threads; *most gets that of all.
+// The largest value of the CTA's earlier threads, 0 where there is none above it; *most gets that of all threads.
 __device__ __forceinline__ int block_max(int v, ScanRoom &room, uint32_t &turn, int *most) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int *top = room.top[turn++ & 1];
@@ -146,10 +146,11 @@ __device__ __forceinline__ int block_max(int v, ScanRoom &room, uint32_t &turn, 
     if (lane >= o) v = max(v, u);
   }
   if (lane == 31) top[warp] = v;
+  const int before = __shfl_up_sync(0xffffffffu, v, 1);
   __syncthreads();
   const int other = top[lane];
   *most = __reduce_max_sync(0xffffffffu, other);
-  return max(v, __reduce_max_sync(0xffffffffu, lane < warp ? other : INT32_MIN));
+  return max(lane > 0 ? before : 0, __reduce_max_sync(0xffffffffu, lane < warp ? other : 0));
 }
 
 struct Cut {  // a unit before it is split
@@ -200,10 +201,10 @@ __global__ void __launch_bounds__(kThreads) prepare_seqs_kernel(const PlanArgs a
   __syncthreads();
   // The sequences, and the units before each.
   unsigned long long total, base = 0;
-  int first = 0;  // largest first row so far
+  int end = 0;  // where the sequences so far end
   for (int b0 = 0; b0 < a.S; b0 += kThreads) {
     const int b = b0 + tid;
-    int u = 0, row = 0;
+    int u = 0, first = 0, last = 0;
     if (b < a.S) {
       const int r0 = a.q_start[b], r1 = a.q_start[b + 1];
       const int kv = a.kv_len != nullptr ? a.kv_len[b] : r1 - r0;
@@ -212,15 +213,16 @@ __global__ void __launch_bounds__(kThreads) prepare_seqs_kernel(const PlanArgs a
       seqs[b] = good ? make_int4(r0, r1 - r0, kv, 0) : make_int4(0, 0, 0, 0);
       if (near) out_seqs[b] = seqs[b];
       u = good ? (r1 - r0 + a.s.unit_tokens - 1) / a.s.unit_tokens : 0;
-      row = good ? r0 : 0;
+      first = good ? r0 : 0;
+      last = good ? r1 : 0;
     }
-    int most_row;
-    row = max(first, block_max(row, room, turn, &most_row));  // a sequence treated as empty starts with its predecessor
-    first = max(first, most_row);
+    int most_end;
+    first = max(first, max(end, block_max(last, room, turn, &most_end)));  // one treated as empty starts where those before it end
+    end = max(end, most_end);
     const unsigned long long before = base + block_scan(u, room, turn, &total);
     if (b < a.S) {
       cum[b] = (int)min(before, (unsigned long long)INT32_MAX);
-      a.plan[a.p.start() + b] = row;
+      a.plan[a.p.start() + b] = first;
     }
     base += total;
   }

@@ -64,6 +64,50 @@ def test_sequences_that_do_not_hold_are_empty(lib, k, what):
     assert what == "falling rows" or torch.equal(s.out, clean)         # (there a cached key of sequence 3 was written over)
 
 
+@pytest.mark.parametrize("bad", [[1], [2, 3], [0], [4], [0, 2, 4]])
+def test_neighbours_of_sequences_that_do_not_hold_are_written(lib, bad):
+    """Their rows belong to nobody; those of the sequences before and behind them go to the cache as ever."""
+    s = Step(8, 2, 64, [5, 1, 3, 0, 7], [40, 9, 0, 16, 2], seed=25)
+    kv = s.kv.copy()
+    kv[bad] = -1
+    s.seqs.prepare(s.T, s.q_start, torch.from_numpy(kv).cuda(), s.table)
+    kc, vc = s.kc.clone(), s.vc.clone()
+    s.write()
+    assert status(lib, s) == (lib.LORA_EBADSEQ, len(bad))
+    table = s.table.cpu().numpy()
+    for b in range(5):
+        if b not in bad:
+            p = np.arange(s.before[b], s.kv[b])
+            rows = slice(int(s.start[b]), int(s.start[b + 1]))
+            for new, cache in ((s.k, kc), (s.v, vc)):
+                cache[torch.from_numpy(table[b, p // s.page]).long().cuda(), torch.from_numpy(p % s.page).cuda()] = new[rows].reshape(-1, 2, 64)
+    assert torch.equal(s.kc.nan_to_num(3.0), kc.nan_to_num(3.0)) and torch.equal(s.vc.nan_to_num(3.0), vc.nan_to_num(3.0))
+
+
+@pytest.mark.parametrize("heads, new, before", [
+    pytest.param((8, 2, 64), [1] * 1500, [i % 37 for i in range(1500)], id="few"),
+    pytest.param((4, 2, 64), [1 + 97 * (i % 29 == 0) for i in range(1100)], [i % 150 for i in range(1100)], id="drafts"),
+    pytest.param((8, 1, 64), [65 + i % 3 for i in range(1030)], [200 * (i % 100 == 7) for i in range(1030)], id="tiles"),
+    pytest.param((2, 2, 40), [i % 3 for i in range(1100)], [5 * (i % 4) for i in range(1100)], id="cores")])
+def test_more_sequences_than_a_plan_keeps_at_hand(lib, heads, new, before):
+    s = Step(*heads, new, before, page=8, seed=26, pad_rows=3)
+    s.write()
+    s.paged()
+    s.check()
+
+
+@pytest.mark.parametrize("heads", [(4, 1, 128), (8, 2, 64)], ids=str)
+def test_units_of_one_tile_ahead_of_units_of_two(lib, heads):
+    """A CTA's first blocks are one stream's alone, its next both streams'. (Beside a long sequence the plan does not tell
+    the costs of short ones apart, so that they come in any order.)"""
+    r = np.random.default_rng(27)
+    new = [64] + [int(r.choice([1, 20, 64, 40])) for _ in range(600)]
+    s = Step(*heads, new, [70000] + [int(r.choice([0, 0, 130, 250])) for _ in range(600)], page=64, seed=27)
+    s.write()
+    s.paged()
+    s.check()
+
+
 @pytest.mark.parametrize("k", KERNELS)
 def test_page_ids_outside_the_cache(lib, k):
     """Their keys count as zeros, nothing is written through them, and both are reported."""
@@ -107,6 +151,23 @@ def test_unseen_values_of_drafts(lib, heads, value):
             assert torch.equal(s.out[a:b], clean[a:b])
         got = s.out[last]
         assert torch.isnan(got).all() if value != value else (got == value).all()
+
+
+@pytest.mark.parametrize("k", KERNELS + [pytest.param(dict(heads=(32, 8, 128), new=[1] * 4), id="decode")])
+@pytest.mark.parametrize("times", [64.0, float("inf"), float("nan")])
+def test_other_sequences_do_not_reach_a_result(lib, k, times):
+    """Bitwise: neither through the softmax's base, which large scores of others would raise."""
+    s = step(k, before=(300, 700, 0, 500))
+    s.write()
+    s.paged()
+    out, lse = s.out.clone(), s.lse.clone()
+    for b in (0, 2):
+        s.q[int(s.start[b]):int(s.start[b + 1])] *= times
+    s.paged()
+    torch.cuda.synchronize()
+    for b in (1, 3):
+        r = slice(int(s.start[b]), int(s.start[b + 1]))
+        assert torch.equal(s.out[r], out[r]) and torch.equal(s.lse[r], lse[r])
 
 
 def test_large_scores_of_few_rows(lib):
