@@ -3,7 +3,7 @@
 Each translation unit under ``csrc/`` compiles in parallel to an object in
 ``<repo>/_build/``; the objects link into ``_lib/librank_adapter_gb300.so``
 inside this package, next to the binding that loads it. The native marshalling
-of the mixture-of-experts calls (``binding/moe_binding.cpp``) compiles beside
+of the mixture-of-experts and attention calls (``binding/moe_binding.cpp``) compiles beside
 them with g++ against the headers of Python and of the installed torch, and
 links to the library as ``_lib/_moe_binding.so``. A rebuild happens only when a
 source or header is newer than what was built, or, for the binding, when torch or
