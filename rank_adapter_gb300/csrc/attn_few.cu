@@ -19,7 +19,7 @@
 // of an SM with three (heads of 64: six) blocks in flight each, so that one's waits and
 // ends of units are the other's time (five requests of 21 thousand keys, 20 heads of 64:
 // 123 us with one warp for all MMAs, 119 with two, 89 with two CTAs; 232 requests of a few
-// keys by 8 heads of 128 34, 34 and 20 us).
+// keys by 8 heads of 128 34, 34 and 22 us).
 #include "attn_tc.cuh"
 
 namespace ra {

@@ -9,10 +9,12 @@
 // units; where there are few, 32 sizes around it are tried, a warp each, and the one
 // is taken whose rounds of CTAs end first (three sequences of 110 thousand keys: 168
 // pieces of a share on 152 CTAs 299 us, 144 larger ones 213). One CTA does it
-// all; it is latency, which a step pays once for all layers.
+// all; it is latency, which a step pays once for all layers: 6.3 us for 256 single tokens,
+// 8.3 for 48 drafts, 14 for those three long ones.
 //
 // Cache write: a warp a row, all of its 16-byte loads in flight before the first
-// store; it moves each byte once in and once out.
+// store; it moves each byte once in and once out (16 prompts of 128 to 2048 tokens, 162
+// MB: 27.2 us, 5.96 TB/s; 256 single tokens 2.9 us with the host's call).
 #include "attn.cuh"
 #include "tcgen05.cuh"
 
