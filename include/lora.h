@@ -634,10 +634,12 @@ int lora_kv_write(const lora_seqs *seqs, const lora_kv_cache *cache, const void 
  *   lse = m + log(sum_j exp(s_j - m))
  * A row that sees no key gets out = 0 and lse = -infinity. Scores, maxima and
  * sums are fp32; on the tensor cores a weight is rounded to bf16 before it
- * multiplies v (not in the sum), which is off by at most 2^-8 of it; out is
- * rounded once. Keys and values that a row does not see do not reach it, NaN
- * and infinity among them. Results do not depend on other sequences' values
- * and repeat bitwise on the same plan and device.
+ * multiplies v (not in the sum), which is off by at most 2^-8 of it (2^-16
+ * where sequences have up to 32 rows of a key-value head on average, tokens
+ * by query heads: single tokens and short drafts); out is rounded once. Keys
+ * and values that a row does not see do not reach it, NaN and infinity among
+ * them. Results do not depend on other sequences' values and repeat bitwise
+ * on the same plan and device.
  *   q, out: device, [num_tokens, num_heads * head_dim], row strides ldq, ldo
  *   k, v:   device, [num_tokens, num_kv_heads * head_dim], row strides ldk, ldv
  *   lse:    device fp32 [num_tokens, num_heads] contiguous, or NULL

@@ -6,7 +6,11 @@
 // its short one, so that little is computed for rows that are not there, and shared memory
 // goes to blocks in flight, 160 to 192 KB of an SM:
 //   S^T = K Q^T     128 keys by N, in TMEM, a thread a key
-//   P^T = 2^(c S^T - m)    bf16, to shared memory, a thread its key's N weights
+//   P^T = 2^(c S^T - m)    to shared memory, a thread its key's N weights, each as a bf16 and
+//                   the bf16 of what that leaves, so that it is off by 2^-16 at most and
+//                   outputs are as good as fp32's (256 requests of up to 4000 keys, 32/8
+//                   heads of 128: 319 us, 312 with one bf16, which over 100 thousand keys
+//                   is off by 0.0020 of the outputs' norm, as much as their own rounding)
 //   O^T += V^T P^T  128 elements of the head by N, in TMEM, a thread an element (a head of
 //                   64 leaves the other 64 rows to whatever lies behind the block)
 // The base m of a row is common to its keys. It need not be their largest score: fp32 and
@@ -18,8 +22,8 @@
 // Scores and products are issued by a warp each. Units of 16 rows leave room for two CTAs
 // of an SM with three (heads of 64: six) blocks in flight each, so that one's waits and
 // ends of units are the other's time (five requests of 21 thousand keys, 20 heads of 64:
-// 123 us with one warp for all MMAs, 119 with two, 89 with two CTAs; 232 requests of a few
-// keys by 8 heads of 128 34, 34 and 22 us).
+// 123 us with one warp for all MMAs, 119 with two, 89 with two CTAs, 95 with the weights'
+// second bf16; 232 requests of a few keys by 8 heads of 128 34, 34, 20 and 22 us).
 #include "attn_tc.cuh"
 
 namespace ra {
@@ -38,8 +42,8 @@ struct FewShape {
   // CTAs of an SM: two, with half of the blocks in flight each, where that leaves room for enough of them.
   static constexpr int kCtas = N == 16 ? 2 : 1;
   static constexpr uint32_t kK = N == 16 ? (D == 64 ? 3 : 2) : (D == 64 ? 6 : 3), kV = N == 16 ? (D == 64 ? 3 : 1) : D == 64 ? 5 : N == 64 ? 2 : 3;
-  static constexpr uint32_t kQ = N == 16 && D == 128 ? 1 : 2, kP = N == 64 || (N == 16 && D == 128) ? 1 : 2;
-  static constexpr int kQHalf = N * 128, kQBytes = kHalves * kQHalf, kPBytes = kKeys * N * 2;
+  static constexpr uint32_t kQ = N == 64 || (N == 16 && D == 128) ? 1 : 2, kP = 1;
+  static constexpr int kQHalf = N * 128, kQBytes = kHalves * kQHalf, kPPart = kKeys * N * 2, kPBytes = 2 * kPPart;
   static constexpr uint32_t kPLayout = N == 16 ? kSw32 : N == 32 ? kSw64 : kSw128;
   static constexpr int kKOff = 0, kVOff = kKOff + (int)kK * kTileBytes, kQOff = kVOff + (int)kV * kTileBytes;
   static constexpr int kPOff = kQOff + (int)kQ * kQBytes;
@@ -261,11 +265,17 @@ __global__ void __launch_bounds__(kThreads, (FewShape<N, D>::kCtas)) attn_few_ke
         tc_after_sync();
         const uint64_t vs = vd + slot * (S::kTileBytes >> 4), pp = pd + ps * (S::kPBytes >> 4);
         if (keys >= kKeys) {
-          mma_run<4>(tmem + S::kO, vs, pp, 128, 2 * N, id_o, b > 0);
-          mma_run<4>(tmem + S::kO, vs + 4 * 128, pp + 8 * N, 128, 2 * N, id_o, 1);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mma_run<4>(tmem + S::kO, vs, pp + i * (S::kPPart >> 4), 128, 2 * N, id_o, b > 0 || i > 0);
+            mma_run<4>(tmem + S::kO, vs + 4 * 128, pp + i * (S::kPPart >> 4) + 8 * N, 128, 2 * N, id_o, 1);
+          }
         } else {
 #pragma unroll 1
-          for (int s = 0; s * 16 < keys; ++s) mma_run<1>(tmem + S::kO, vs + s * 128, pp + s * 2 * N, 0, 0, id_o, b > 0 || s > 0);
+          for (int s = 0; s * 16 < keys; ++s) {
+            mma_run<1>(tmem + S::kO, vs + s * 128, pp + s * 2 * N, 0, 0, id_o, b > 0 || s > 0);
+            mma_run<1>(tmem + S::kO, vs + s * 128, pp + (S::kPPart >> 4) + s * 2 * N, 0, 0, id_o, 1);
+          }
         }
         mma_commit_elect(&pfree[ps]);
         mma_commit_elect(&vfree[slot]);
@@ -365,15 +375,19 @@ __global__ void __launch_bounds__(kThreads, (FewShape<N, D>::kCtas)) attn_few_ke
         unsigned char *row = sm + S::kPOff + (g % S::kP) * S::kPBytes + tid * (2 * N);
 #pragma unroll
         for (int x = 0; x < N; x += 8) {
-          uint32_t p[4];
+          uint32_t p[4], rest[4];
 #pragma unroll
           for (int y = 0; y < 8; y += 2) {
             const float p0 = ex2(fmaf(s[x + y], c, -base[x + y])), p1 = ex2(fmaf(s[x + y + 1], c, -base[x + y + 1]));
             l[x + y] += p0;
             l[x + y + 1] += p1;
-            p[y / 2] = pack_bf16(p0, p1);
+            const uint32_t both = pack_bf16(p0, p1);
+            p[y / 2] = both;
+            rest[y / 2] = pack_bf16(p0 - __uint_as_float(both << 16), p1 - __uint_as_float(both & 0xffff0000u));
           }
-          *reinterpret_cast<uint4 *>(row + ((x / 8) ^ swz) * 16) = make_uint4(p[0], p[1], p[2], p[3]);
+          uint4 *to = reinterpret_cast<uint4 *>(row + ((x / 8) ^ swz) * 16);
+          to[0] = make_uint4(p[0], p[1], p[2], p[3]);
+          to[S::kPPart / 16] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
         }
         fence_async_smem();
         tc_before_sync();

@@ -177,6 +177,21 @@ def test_large_scores_of_few_rows(lib):
     s.check()
 
 
+@pytest.mark.parametrize("new", [[1] * 6, [4, 3, 4, 3, 4, 3]], ids=str)
+@pytest.mark.parametrize("heads", [(8, 2, 128), (8, 2, 64), (16, 2, 128), (16, 2, 64), (28, 4, 128), (64, 1, 64), (64, 1, 128), (14, 2, 64)], ids=str)
+def test_weights_of_few_rows_are_two_bf16(lib, heads, new):
+    """Off by half a step of half a step: (2^-8)^2 = 2^-16 of a weight, beside the output's own rounding. With more than 32
+    rows of a key-value head a sequence on average they are one bf16."""
+    s = Step(*heads, new, [3000, 1, 0, 700, 127, 5000], page=32, seed=28)
+    few = s.used * heads[0] // heads[1] <= 32 * len(new)
+    s.write()
+    s.paged()
+    s.check()
+    out, lse, spread, reach = s.oracle()
+    tol, _ = attn_oracle.tolerance(out, lse, spread, reach, s.D, int(s.kv.max()), 2.0 ** -16 if few else 2.0 ** -8, 2.0 ** -8)
+    assert (np.abs(f64(s.out).reshape(out.shape) - out) <= tol).all()
+
+
 @pytest.mark.parametrize("heads,new", [((4, 2, 128), [3] * 9), ((2, 1, 64), [1, 9, 0, 2]), ((64, 1, 64), [1] * 5), ((8, 8, 128), [2, 31])], ids=str)
 def test_short_prompts(lib, heads, new):
     s = Step(*heads, new, seed=24, pad_rows=2)
