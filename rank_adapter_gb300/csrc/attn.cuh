@@ -104,7 +104,7 @@ cudaError_t launch_kv_write(const lora_seqs &q, const lora_kv_cache &c, const vo
                             int64_t ldv, cudaStream_t st);
 bool attn_tc_takes(const AttnShape &s);
 cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t st);       // tensor cores (attn_tc.cu)
-cudaError_t launch_attn_few(const AttnArgs &a, cudaStream_t st);      // the same, units of few rows over pages (attn_few.cu)
+cudaError_t launch_attn_few(const AttnArgs &a, cudaStream_t st);      // the same, units of few rows (attn_few.cu)
 cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t st);     // CUDA cores (attn_rows.cu)
 cudaError_t launch_attn_combine(const AttnArgs &a, cudaStream_t st);  // joins the partial results
 

@@ -32,17 +32,6 @@ __device__ __forceinline__ void mma_pv4(uint32_t d, uint32_t p, uint64_t bd, uin
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}"
       ::"r"(d), "r"(p), "l"(bd), "r"(idesc), "r"(acc), "l"(b_step) : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
-      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
-        "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
@@ -158,10 +147,9 @@ struct Walk {
     fetch();
     return true;
   }
-  __device__ __forceinline__ void done(const Item &it) { done(it.blocks); }
-  __device__ __forceinline__ void done(int blocks) {
-    pos += blocks;
-    index += blocks > 0;
+  __device__ __forceinline__ void done(const Item &it) {
+    pos += it.blocks;
+    index += it.blocks > 0;
   }
   // Stream t's blocks of the item: from first(t) on, every step(it)-th one.
   __device__ __forceinline__ int first(const Item &it, int t) const { return it.pair ? 0 : (int)((pos ^ (uint32_t)t) & 1u); }
